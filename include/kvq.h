@@ -150,7 +150,8 @@ enum {
   KVQ_FAULT_CONTEXT = 4,     /* context length outside [0, max_context] or the table */
   KVQ_FAULT_SEQ = 8,         /* sequence id outside [0, max_seqs) */
   KVQ_FAULT_INT4_RUN = 16,   /* INT4 page rows not one whole, ordered block */
-  KVQ_FAULT_TIMEOUT = 32     /* a bounded wait inside a kernel ran out */
+  KVQ_FAULT_TIMEOUT = 32,    /* a bounded wait inside a kernel ran out */
+  KVQ_FAULT_TREE = 64        /* kvq_tree_commit: path not increasing, or outside its tree */
 };
 
 /*
@@ -417,6 +418,179 @@ kvq_status kvq_decode_attention_noalloc(const kvq_cache_desc* cache, const void*
                                         const int32_t* seq_ids, int max_context,
                                         float softmax_scale, void* out, int32_t out_dtype,
                                         cudaStream_t stream);
+
+/*
+ * Rotary position embedding (none of the pages mentions it; a model whose keys are rotated
+ * rotates them before they are written, which kvq_rope_write fuses with the write).
+ *   Pair p < rot_dim/2 of a head at position t turns by the angle t * f_p:
+ *     (a, b) -> m * (a cos - b sin, b cos + a sin),
+ *   (a, b) = (x[p], x[p + rot_dim/2]) for KVQ_ROPE_HALF, (x[2p], x[2p+1]) for
+ *   KVQ_ROPE_INTERLEAVED; x[rot_dim..] passes through unchanged (m does not apply to it).
+ *   Angles are formed in float64, so positions up to 2^31 keep float32 accuracy.
+ */
+typedef enum { KVQ_ROPE_HALF = 0, KVQ_ROPE_INTERLEAVED = 1 } kvq_rope_layout;
+
+/*
+ * How frequencies are stretched for contexts longer than the trained one; f_p below is the
+ * unscaled theta^(-2p/rot_dim), s = factor, n = original_context:
+ *   NONE        f_p
+ *   LINEAR      f_p / s                        (positions interpolated)
+ *   NTK         theta'^(-2p/rot_dim), theta' = theta * s^(rot_dim/(rot_dim-2))
+ *   WAVELENGTH  with t = n f_p / 2 pi turns within the original context: f_p where
+ *               t >= high, f_p / s where t <= low, linear in t between them
+ *   YARN        with c(t) = rot_dim ln(n / 2 pi t) / 2 ln theta the pair that makes t turns:
+ *               f_p for p <= floor(c(high)), f_p / s for p >= ceil(c(low)), linear in p between
+ *               them; m = 0.1 ln(s) + 1 (B. Peng et al., "YaRN", arXiv 2309.00071)
+ */
+typedef enum {
+  KVQ_ROPE_SCALE_NONE = 0,
+  KVQ_ROPE_SCALE_LINEAR = 1,
+  KVQ_ROPE_SCALE_NTK = 2,
+  KVQ_ROPE_SCALE_WAVELENGTH = 3,
+  KVQ_ROPE_SCALE_YARN = 4
+} kvq_rope_scaling;
+
+/*
+ *   rot_dim           rotated dimensions of a head, even, at most head_dim; the kernels take
+ *                     multiples of 16 (others: KVQ_ERR_UNSUPPORTED).
+ *   original_context, low, high   WAVELENGTH and YARN only; 0 < low < high.
+ *   attention_factor  m; 0 selects the scaling's own (1, or YaRN's).
+ */
+typedef struct {
+  int32_t layout;
+  int32_t rot_dim;
+  int32_t scaling;
+  int32_t original_context;
+  double theta;
+  double factor;
+  double low;
+  double high;
+  double attention_factor;
+} kvq_rope_desc;
+
+/*
+ * kvq_rope_frequencies - the frequencies f_p (radians per position) of a rope descriptor and
+ *   its factor m.  Host only.  freqs is a HOST float64 [rot_dim/2] (or NULL), attention_factor
+ *   a host float64 (or NULL).  The caller copies the frequencies to the device once; a caller
+ *   with frequencies of its own (a list of per-pair factors, say) passes those instead.
+ */
+kvq_status kvq_rope_frequencies(const kvq_rope_desc* rope, double* freqs, double* attention_factor);
+
+/*
+ * kvq_rope - rotate query and key rows.
+ *   freqs         float64 [rot_dim/2], device (the descriptor's scaling fields give m only).
+ *   act_dtype     BF16 or FP16; head_dim 64 or 128.
+ *   positions     int32 [num_tokens], device; any value (a negative one turns backwards,
+ *                 which is also the gradient of the rotation).
+ *   q, k          act_dtype [num_tokens][heads][head_dim], device, tokens q_stride / k_stride
+ *                 elements apart (multiples of 8, at least heads * head_dim: rows of a fused
+ *                 projection are taken as they are).  With 0 heads the tensor is not looked at.
+ *   q_out, k_out  the same shapes with strides of their own; an output may be its own input
+ *                 (same pointer and stride), but may not overlap it otherwise.
+ *   Values are rotated in float32 and rounded once to act_dtype.
+ */
+kvq_status kvq_rope(const kvq_rope_desc* rope, const double* freqs, int32_t act_dtype, int head_dim,
+                    const int32_t* positions, int num_tokens, const void* q, int64_t q_stride,
+                    int num_q_heads, void* q_out, int64_t q_out_stride, const void* k,
+                    int64_t k_stride, int num_kv_heads, void* k_out, int64_t k_out_stride,
+                    cudaStream_t stream);
+
+/*
+ * kvq_rope_write - kvq_rope of q and k, and kvq_write of the rotated k and of v, in one launch.
+ *   k_new, v_new  act_dtype [num_tokens][H][D], token strides k_stride, v_stride as above.
+ *   slot_mapping  int32 [num_tokens], device, as kvq_write: slot -1 stores no K / V row (its
+ *                 q row is rotated all the same).
+ *   q may have 0 heads.  The quantizers take the rotated float32 values: for quantized caches
+ *   K is not rounded to act_dtype in between (for 16-bit caches the stored rows equal kvq_rope
+ *   then kvq_write).  V rows are stored exactly as kvq_write stores them.
+ *   Dense caches (INT4 / INT2: KVQ_ERR_UNSUPPORTED; use kvq_rope, then kvq_write).
+ */
+kvq_status kvq_rope_write(const kvq_cache_desc* cache, const kvq_rope_desc* rope,
+                          const double* freqs, const int32_t* positions, int num_tokens,
+                          const void* q, int64_t q_stride, int num_q_heads, void* q_out,
+                          int64_t q_out_stride, const void* k_new, int64_t k_stride,
+                          const void* v_new, int64_t v_stride, const int32_t* slot_mapping,
+                          cudaStream_t stream);
+
+/*
+ * kvq_gather - read cached rows back by slot (the counterpart of kvq_write).
+ *   slots         int32 [num_rows], device: cache slot of each row.  -1 leaves the output row as
+ *                 it was, and so does a slot out of range (counted, KVQ_FAULT_SLOT).
+ *   k_out, v_out  act_dtype [num_rows][H][D], device: the dequantized values of the header
+ *                 comment, formed in float32 and rounded once to act_dtype (16-bit caches: the
+ *                 stored bits).
+ *   Every cache type; for INT4 / INT2 rows of blocks only (the residual ring has no slots).
+ */
+kvq_status kvq_gather(const kvq_cache_desc* cache, const int32_t* slots, int num_rows, void* k_out,
+                      void* v_out, cudaStream_t stream);
+
+/*
+ * Workspace bytes kvq_tree_attention needs for this shape (host only, as
+ * kvq_decode_workspace_size).  May be 0.
+ */
+kvq_status kvq_tree_workspace_size(const kvq_cache_desc* cache, int batch, int num_q_heads,
+                                   int max_tree, int max_context, size_t* bytes);
+
+/*
+ * kvq_tree_attention - attention of a tree of drafted tokens per sequence (speculative
+ *   decoding): the drafted tokens' K / V rows are already in the cache, as the newest
+ *   positions of their sequence, and each attends to the cached prefix and to the drafted
+ *   tokens that its mask row names (its ancestors and itself).
+ *   q             act_dtype [num_q_tokens][num_q_heads][D], device: the drafted tokens of sequence b
+ *                 are rows q_start[b] .. q_start[b+1]-1, in the order of their cache positions.
+ *   q_start       int32 [batch+1], device.
+ *   max_tree      host upper bound of a sequence's drafted tokens, at most 1024.
+ *   tree_mask     uint32 [num_q_tokens][mask_words], device, mask_words >= ceil(max_tree/32): bit
+ *                 j % 32 of word j / 32 of row i says whether query i sees drafted token j of its
+ *                 sequence.  Nothing is implied: a token sees itself only if its own bit is
+ *                 set.  Bits past the sequence's drafted tokens are ignored.
+ *   context_lens  int32 [batch], device: cached positions of sequence b, the L_b drafted ones
+ *                 included; drafted token j is position context_lens[b] - L_b + j.
+ *   out           out_dtype [num_q_tokens][num_q_heads][D], device.  A query that sees nothing
+ *                 (no prefix, no bit) gets zeros.  Rows of no sequence are left as they were, and
+ *                 so are those of a sequence that is rejected and counted
+ *                 (KVQ_FAULT_CONTEXT): more drafted tokens than positions or than max_tree, a
+ *                 context length outside [0, max_context] or the block table, query rows outside
+ *                 [0, num_q_tokens].
+ *   workspace     as kvq_decode_attention: kvq_tree_workspace_size() bytes, no initialisation,
+ *                 not shared by calls that overlap on the GPU.
+ *   Positions on a block id out of range are left out (counted, KVQ_FAULT_BLOCK).  Infinities and
+ *   NaN in drafted rows reach only the queries that see them.  With one drafted token that sees
+ *   itself the result is kvq_decode_attention's.
+ *   Dense caches.  head_dim 128 with block_size 16 (not PER_CHANNEL) runs on the 5th-generation
+ *   tensor cores, any GQA group; other geometries on a CUDA-core kernel.  With BF16 output and
+ *   8-bit or FP16 caches the tensor-core kernel rounds the probabilities to fp16 (2^-12 relative,
+ *   an eighth of the output's own half step); otherwise they keep 16 bits or more.
+ *   INT4 / INT2: KVQ_ERR_UNSUPPORTED (a rejected draft could not be taken back out of the ring).
+ */
+kvq_status kvq_tree_attention(const kvq_cache_desc* cache, const void* q, int num_q_tokens,
+                              int batch, int num_q_heads, const int32_t* q_start, int max_tree,
+                              const uint32_t* tree_mask, int mask_words,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, int max_context, float softmax_scale,
+                              void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
+/*
+ * kvq_tree_commit - keep the accepted path of each drafted tree: the cache rows of drafted tokens
+ *   path[b][0 .. accepted[b]-1] move to the first positions of the draft, codes and scales as
+ *   they are, so that the sequence then has context_lens[b] - L_b + accepted[b] positions.
+ *   path          int32 [batch][max_accept], device: drafted indexes, strictly increasing, each
+ *                 below L_b = q_start[b+1] - q_start[b].
+ *   accepted      int32 [batch], device, in [0, min(L_b, max_accept)].
+ *   context_lens  int32 [batch], device: as for kvq_tree_attention (before the commit).
+ *   new_lens      int32 [batch], device, or NULL: receives the new context lengths; not
+ *                 context_lens itself.
+ *   Positions behind the new length keep their bytes.  A sequence with a length or count out of
+ *   range (KVQ_FAULT_CONTEXT), or whose path is not increasing, leaves its tree or meets a block
+ *   id out of range (KVQ_FAULT_TREE), is counted, moves nothing and keeps context_lens[b].
+ *   Two sequences must not share blocks that hold drafted positions.
+ *   Dense caches (INT4 / INT2: KVQ_ERR_UNSUPPORTED).
+ */
+kvq_status kvq_tree_commit(const kvq_cache_desc* cache, const int32_t* path, int max_accept,
+                           const int32_t* accepted, int batch, const int32_t* q_start,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, int32_t* new_lens, cudaStream_t stream);
 
 /*
  * kvq_dequant - debug: expand whole blocks back to float32.

@@ -87,3 +87,32 @@ def prefill_attention(cache, q, q_start, block_tables, context_lens, softmax_sca
                 out[qs[b] + i, hq] = softmax_attention(q[qs[b] + i, hq], K[kvh][:p + 1],
                                                        V[kvh][:p + 1], scale)
     return out
+
+
+def tree_attention(cache, q, q_start, sees, block_tables, context_lens, softmax_scale=0.0):
+    """Attention of drafted trees over the dequantized cache, float64.
+
+    q [Tq, H_q, D]; the drafted tokens of sequence b are rows q_start[b] .. q_start[b+1]-1, the
+    newest positions of that sequence (n_b = context_lens[b], L_b drafted).  sees[i] is the list
+    of drafted indexes query row i sees; it also sees every position below n_b - L_b.  A query
+    that sees nothing gives zeros.  Returns (out, spread), both [Tq, H_q, D]; spread is
+    sum_p w_p |v_p|, what rounding errors of the weights scale with.
+    """
+    q = np.asarray(q, np.float64)
+    Tq, Hq, D = q.shape
+    g = Hq // cache.H
+    scale = softmax_scale if softmax_scale else 1.0 / np.sqrt(D)
+    out, spread = np.zeros((Tq, Hq, D)), np.zeros((Tq, Hq, D))
+    for b in range(len(context_lens)):
+        n, first = int(context_lens[b]), int(q_start[b])
+        L = int(q_start[b + 1]) - first
+        if L == 0:
+            continue
+        K, V = cache.gather(block_tables[b], n)
+        for i in range(L):
+            at = list(range(n - L)) + [n - L + j for j in sorted(sees[first + i]) if j < L]
+            for hq in range(Hq):
+                k, v = K[hq // g][at], V[hq // g][at]
+                out[first + i, hq] = softmax_attention(q[first + i, hq], k, v, scale)
+                spread[first + i, hq] = softmax_attention(q[first + i, hq], k, np.abs(v), scale)
+    return out, spread

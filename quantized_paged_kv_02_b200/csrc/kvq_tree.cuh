@@ -1,0 +1,105 @@
+// Shared by the tree-attention sources: parameters, per-sequence bounds, the visibility bits
+// of a query, the block-balanced schedule and the split plan.
+#pragma once
+
+#include "kvq_internal.cuh"
+
+namespace kvq {
+
+constexpr int kTreeMax = 1024;       // drafted tokens per sequence at most
+constexpr int kTreeRows = 128;       // tensor-core kernel: query rows per tile
+constexpr int kTreeBlk = 128;        // ... and cached tokens per block
+
+struct TreePlan {
+  int kernel;          // 0 CUDA cores, 1 tensor cores (tcgen05)
+  int g;               // query heads per kv head
+  int splits, chunk;   // kernel 0: token splits, tokens each
+  int ctas;            // kernel 1: persistent CTAs
+  size_t ws_bytes, ws_ml_off;
+};
+
+struct TreeParams {
+  const void* q;             // [Tq][Hq][D] act
+  const int32_t* q_start;    // [B+1]
+  const uint32_t* mask;      // [Tq][mask_words]
+  const int32_t* tables;     // [B][max_blocks]
+  const int32_t* lens;       // [B]
+  int Tq, B, H, Hq, g, D;
+  int max_tree, mask_words, max_blocks, max_context;
+  const uint8_t* pages;
+  const float* k_static;
+  const float* v_static;
+  int NB, bs, record, off_v, off_s, row_bytes, mode, cache_dtype, act_fp16;
+  float scale_log2;
+  void* out;
+  int out_dtype;
+  int splits, chunk, ctas;
+  float* ws_o;
+  float* ws_ml;
+  int32_t* fault;
+};
+
+// Sequence b: its query rows start at q0, L drafted tokens, n cached positions (the drafted
+// ones last).  L = 0 for a sequence without queries or one that is rejected: a context length
+// outside [0, max_context] or the block table, more queries than positions or than max_tree,
+// or query rows outside [0, Tq].
+struct TreeSeq {
+  int q0, L, n;
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b, bool report = false) {
+  TreeSeq s;
+  s.q0 = p.q_start[b];
+  const int q1 = p.q_start[b + 1];
+  s.L = q1 - s.q0;
+  s.n = p.lens[b];
+  const bool ok = s.q0 >= 0 && s.L >= 0 && q1 <= p.Tq && s.L <= p.max_tree && s.n >= s.L && s.n <= p.max_context &&
+                  s.n <= static_cast<long>(p.max_blocks) * p.bs;
+  if (!ok) {
+    if (report) record_fault(p.fault, KVQ_FAULT_CONTEXT);
+    s.L = 0;
+  }
+  return s;
+}
+
+// Visibility of the 32 positions from `pos` on to the query whose mask row is `row`: bit i is
+// position pos + i.  Positions below n - L are the prefix (all visible), position n - L + j is
+// drafted token j (bit j of the row), positions from n on are not there.
+__device__ __forceinline__ uint32_t visible32(const uint32_t* row, int pos, int n, int L) {
+  const int j0 = pos - (n - L);                  // drafted index of the first position
+  if (j0 + 32 <= 0) return 0xFFFFFFFFu;
+  uint32_t w = 0;
+  if (j0 < L) {
+    const int words = (L + 31) >> 5;
+    if (j0 >= 0) {
+      const int k = j0 >> 5, sh = j0 & 31;
+      w = row[k] >> sh;
+      if (sh != 0 && k + 1 < words) w |= row[k + 1] << (32 - sh);
+    } else {
+      w = (row[0] << -j0) | ((1u << -j0) - 1u);  // the prefix part below the draft
+    }
+    const int have = L - j0;                     // positions of the word that exist
+    if (have < 32) w &= (1u << have) - 1u;
+  }
+  return w;
+}
+
+// Block-balanced schedule of the tensor-core kernel.  A unit is one (sequence, kv head, tile of
+// 128 query rows) and has ceil(n / 128) blocks; the blocks of all units, in the order
+// (sequence, kv head, tile), are cut into ctas contiguous ranges.  A CTA has at most two
+// segments that do not hold a whole unit: one that does not begin its unit (partial slot
+// 2 c) and one that begins but does not end it (slot 2 c + 1).
+__device__ __forceinline__ int tree_tiles(const TreeParams& p, int L) {
+  return (L * p.g + kTreeRows - 1) / kTreeRows;
+}
+__device__ __forceinline__ int tree_blocks(int n) { return (n + kTreeBlk - 1) / kTreeBlk; }
+__device__ __forceinline__ long long tree_work(const TreeParams& p, const TreeSeq& s) {
+  return s.L > 0 ? static_cast<long long>(tree_tiles(p, s.L)) * p.H * tree_blocks(s.n) : 0;
+}
+__device__ __forceinline__ long long tree_range(long long W, int c, int C) { return W * c / C; }
+
+bool tree_tc_supported(const Geometry& g, int group);
+cudaError_t launch_tree_simt(const TreeParams& p, int act, cudaStream_t s);
+cudaError_t launch_tree_tc(const TreeParams& p, const Geometry& g, cudaStream_t s);
+
+}  // namespace kvq

@@ -1,0 +1,1069 @@
+// Attention of drafted token trees on the 5th-generation tensor cores (tcgen05.mma,
+// accumulators in tensor memory): head_dim 128, block size 16, INT8 / FP8 / BF16 / FP16 caches.
+//
+// A unit is one tile of 128 query rows (row r: drafted token r / g, head r % g) of one
+// (sequence, kv head); it walks the sequence's positions in blocks of 128.  One persistent CTA
+// per SM takes an equal share of all units' blocks (kvq_tree.cuh), so that a few long
+// sequences and many short ones both fill the machine; a unit cut between CTAs leaves partial
+// results (unnormalised O, exponent offset, sum) that tree_merge_kernel joins.
+//
+// Inside a CTA the blocks go to two streams in turn, each with its own scores, running
+// maximum, sum and output accumulator in tensor memory (S0 S1 O0 O1: all 512 columns), joined
+// once per unit.  So the chain of one block (S = Q K^T, softmax, O += P V) never waits for the
+// softmax of the block before it, and while one stream's warps work on scores the tensor
+// cores work for the other: with few query rows the bound is the cache's bytes, and that
+// needs a block about every 1500 cycles, half of one chain's length.
+//
+//   warps 0-3, 4-7  softmax of stream 0 / 1: one query row per thread;
+//   warp 8          producer: block-table entries, one bulk copy per page record into a ring of
+//                   half blocks (16-bit caches: four TMA tensor copies per page straight into
+//                   the K / V tiles);
+//   warp 9          MMA issuer;
+//   warps 10-13     K converters, 14-17 V converters: codes -> fp16 tiles (exact).
+//
+// Query i sees the prefix and the drafted tokens of its mask row.  Blocks that hold prefix
+// only, on pages that passed their table check, take a path without per-score tests; in the
+// others a 32-bit word per row and 32 positions selects the visible scores (selected, never
+// multiplied: a masked score may be NaN).  P is 0 at masked positions, which P V would still
+// multiply with V: V rows outside the sequence are zeros in the tile, and a drafted row's
+// infinities and NaN are left out of the tile and added in the end to the rows that see
+// them.
+//
+// Rounding: K and V codes are exact in fp16, q is exact in fp16 (bf16 activations: scaled by a
+// power of two per tile).  P is one fp16 (11 bits) when the output is bf16 (8 bits) and the
+// tiles are fp16, which leaves the output's own rounding ten times larger than P's; otherwise
+// P is a hi + lo pair of 16-bit halves (two MMAs).  Scores, sums and O are binary32.
+#include <climits>
+#include <mutex>
+
+#include "kvq_decode_common.cuh"
+#include "kvq_ptx.cuh"
+#include "kvq_tc.cuh"
+#include "kvq_tree.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kD = 128, kBS = 16, kPPB = kTreeBlk / kBS;
+constexpr int kThreads = 576;
+constexpr int kSoftWarps = 8, kProdWarp = 8, kMmaWarp = 9, kConvWarp0 = 10;
+constexpr int kTile = 32768;         // 128 x 128 16-bit elements
+constexpr int kNQ = 4;               // slots of per-block K data
+constexpr float kRebase = 8.f;       // log2 headroom before the running maximum is re-based
+constexpr uint32_t kTmemCols = 512, kTmO = 256;
+
+template <int CD, bool PT>
+struct Layout {
+  static constexpr bool DIRECT = CD == KVQ_DTYPE_BF16 || CD == KVQ_DTYPE_FP16;
+  static constexpr bool BF = CD == KVQ_DTYPE_BF16;              // tile type
+  static constexpr int ROWB = DIRECT ? 2 * kD : kD;
+  static constexpr int OFF_V = kBS * ROWB, OFF_S = 2 * kBS * ROWB;
+  static constexpr int REC = OFF_S + (PT ? 8 * kBS : 0);
+  static constexpr int NB = DIRECT ? 3 : 2;                     // K and V tile buffers each
+  static constexpr int HP = kPPB / 2;                           // pages per half block
+  static constexpr int RH = DIRECT ? 0 : 3;                     // raw ring, in half blocks
+  static constexpr int K_OFF = 0;
+  static constexpr int V_OFF = NB * kTile;
+  static constexpr int Q_OFF = V_OFF + NB * kTile;
+  static constexpr int RAW_OFF = Q_OFF + kTile;
+  static constexpr int KS_OFF = RAW_OFF + RH * HP * REC;        // float [kNQ][128] K scales (PT)
+  static constexpr int VS_OFF = KS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [NB][128]
+  static constexpr int MISC_OFF = VS_OFF + (PT ? NB * kTreeBlk * 4 : 0);
+  // page flags of the raw ring / tile buffers; pok [kNQ]; vmax, nonfinite [NB][4]; amax [8];
+  // schedule [4]; tmem, abort
+  static constexpr int NPOK = DIRECT ? NB * kPPB : RH * HP;
+  static constexpr int WORDS = NPOK + kNQ + 8 * NB + 8 + 6 + 2;
+  static constexpr int BAR_OFF = (MISC_OFF + 4 * WORDS + 7) / 8 * 8;
+  // raw_full, raw_empty [RH]; tile_full [NB] (DIRECT); k_full, k_free, v_full, v_free [NB];
+  // s_full, p_full [2]; kq_full, kq_free [kNQ]; q_ready, o_full, sync, fin
+  static constexpr int NBARS = 2 * RH + 5 * NB + 4 + 2 * kNQ + 4;
+  static constexpr int BYTES = 1024 + BAR_OFF + 8 * NBARS;
+  static_assert(BYTES <= 227 * 1024, "fits the shared memory of one CTA");
+  static_assert(BYTES > 114 * 1024, "one CTA per SM: its TMEM allocation never waits for a peer");
+};
+
+// One segment of the schedule: blocks [j0, j1) of a unit.
+struct Seg {
+  int b, kvh, tile, q0, L, n, nblk, j0, j1;
+};
+
+struct Walk {
+  int b, u, j, tiles;
+  long long left;
+  TreeSeq s;
+  __device__ __forceinline__ void load(const TreeParams& p) {
+    while (b < p.B) {
+      s = tree_seq(p, b);
+      if (s.L > 0) break;
+      ++b;
+    }
+    tiles = s.L > 0 ? tree_tiles(p, s.L) : 1;
+  }
+  __device__ __forceinline__ Walk(const TreeParams& p, const int* sched) {
+    b = sched[0];
+    u = sched[1];
+    j = sched[2];
+    left = sched[3];
+    if (left > 0) load(p);
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p, Seg& g) {
+    if (left <= 0) return false;
+    if (u == p.H * tiles) {
+      u = 0;
+      ++b;
+      load(p);
+    }
+    g.b = b;
+    g.kvh = u / tiles;
+    g.tile = u - g.kvh * tiles;
+    g.q0 = s.q0;
+    g.L = s.L;
+    g.n = s.n;
+    g.nblk = tree_blocks(s.n);
+    g.j0 = j;
+    g.j1 = static_cast<int>(min(static_cast<long long>(g.nblk), j + left));
+    left -= g.j1 - g.j0;
+    j = 0;
+    ++u;
+    return true;
+  }
+};
+
+struct Shared {
+  uint64_t *raw_full, *raw_empty, *tile_full, *k_full, *k_free, *v_full, *v_free, *s_full, *p_full, *kq_full,
+      *kq_free, *q_ready, *o_full, *sync, *fin;
+  int *page_ok, *pok, *vnf, *sched;
+  float *vmax, *amax, *ks, *vs;
+  uint32_t* tmem;
+  volatile int* abort;
+};
+
+// Bounded wait that also gives up when another role has; the thread sleeps in the barrier.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitCycles) return false;
+  }
+  return true;
+}
+
+__device__ __forceinline__ void fail(const TreeParams& p, volatile int* abort) {
+  record_fault(p.fault, KVQ_FAULT_TIMEOUT);
+  *abort = 1;
+}
+
+// Swizzled byte offset of 16-byte chunk c (8 elements, c < 16) of row t in a 128 x 128 tile.
+__device__ __forceinline__ uint32_t tile_off(int t, int c) {
+  return static_cast<uint32_t>((c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4));
+}
+
+__device__ __forceinline__ uint4 i8x8_to_f16(uint2 w) {
+  const uint32_t a = w.x ^ 0x80808080u, b = w.y ^ 0x80808080u;
+  return make_uint4(i8x2_to_f16x2(a, kLoPair), i8x2_to_f16x2(a, kHiPair), i8x2_to_f16x2(b, kLoPair),
+                    i8x2_to_f16x2(b, kHiPair));
+}
+
+__device__ __forceinline__ uint4 e4m3x8_to_f16(uint2 w) {
+  return make_uint4(e4m3x2_to_f16x2(w.x & 0xFFFFu), e4m3x2_to_f16x2(w.x >> 16),
+                    e4m3x2_to_f16x2(w.y & 0xFFFFu), e4m3x2_to_f16x2(w.y >> 16));
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float2 w) {
+  return BF ? pack_bf16x2(w.x, w.y) : pack_f16x2(w.x, w.y);
+}
+
+// hi + lo split of two values into 16-bit pairs.
+template <bool BF>
+__device__ __forceinline__ void split2(float2 w, uint32_t& hi, uint32_t& lo) {
+  hi = pack2<BF>(w);
+  float2 h;
+  if constexpr (BF) h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi));
+  else h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  lo = pack2<BF>(__fadd2_rn(w, make_float2(-h.x, -h.y)));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+  st8(taddr, r);
+  st8(taddr + 8, r + 8);
+}
+
+// 16-bit pairs of w whose exponent is all ones (infinity, NaN) set to zero; true if any was.
+template <bool BF>
+__device__ __forceinline__ bool drop_nonfinite(uint4& u) {
+  constexpr uint32_t e = BF ? 0x7F80u : 0x7C00u;
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t& w = (&u.x)[i];
+    if ((w & e) == e) { w &= 0xFFFF0000u; any = true; }
+    if (((w >> 16) & e) == e) { w &= 0xFFFFu; any = true; }
+  }
+  return any;
+}
+
+// Visibility of a row's columns [32 i, 32 i + 32) of block j: its mask bits, without the tokens
+// of pages that failed their check (bit pp of pok: page pp of the block is there).
+__device__ __forceinline__ uint32_t column_bits(const uint32_t* row, int pok, int j, int i, int n, int L) {
+  const uint32_t pages = ((pok >> (2 * i)) & 1 ? 0xFFFFu : 0u) | ((pok >> (2 * i + 1)) & 1 ? 0xFFFF0000u : 0u);
+  return visible32(row, j * kTreeBlk + 32 * i, n, L) & pages;
+}
+
+template <int CD, bool PT, bool HILO>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap rows) {
+  using Y = Layout<CD, PT>;
+  constexpr bool BF = Y::BF, DIRECT = Y::DIRECT;
+  constexpr int NB = Y::NB;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Shared sh;
+  {
+    int* w = reinterpret_cast<int*>(smem + Y::MISC_OFF);
+    sh.page_ok = w;
+    sh.pok = w + Y::NPOK;
+    sh.vnf = sh.pok + kNQ;                                   // [NB][4]
+    sh.vmax = reinterpret_cast<float*>(sh.vnf + 4 * NB);     // [NB][4]
+    sh.amax = sh.vmax + 4 * NB;                              // [8]
+    sh.sched = reinterpret_cast<int*>(sh.amax + 8);          // [6]
+    sh.tmem = reinterpret_cast<uint32_t*>(sh.sched + 6);
+    sh.abort = reinterpret_cast<volatile int*>(sh.sched + 7);
+    sh.ks = reinterpret_cast<float*>(smem + Y::KS_OFF);
+    sh.vs = reinterpret_cast<float*>(smem + Y::VS_OFF);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Y::BAR_OFF);
+    auto take = [&](int n) { uint64_t* r = bar; bar += n; return r; };
+    sh.raw_full = take(Y::RH);
+    sh.raw_empty = take(Y::RH);
+    sh.tile_full = take(NB);
+    sh.k_full = take(NB);
+    sh.k_free = take(NB);
+    sh.v_full = take(NB);
+    sh.v_free = take(NB);
+    sh.s_full = take(2);
+    sh.p_full = take(2);
+    sh.kq_full = take(kNQ);
+    sh.kq_free = take(kNQ);
+    sh.q_ready = take(1);
+    sh.o_full = take(1);
+    sh.sync = take(1);
+    sh.fin = take(1);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Y::RH; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], 8);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&sh.tile_full[i], 1);
+      mbar_init(&sh.k_full[i], 4);
+      mbar_init(&sh.k_free[i], 1);
+      mbar_init(&sh.v_full[i], 4);
+      mbar_init(&sh.v_free[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+    }
+    for (int i = 0; i < kNQ; ++i) {
+      mbar_init(&sh.kq_full[i], 4);
+      mbar_init(&sh.kq_free[i], 4);
+    }
+    mbar_init(sh.q_ready, kSoftWarps);
+    mbar_init(sh.o_full, 1);
+    mbar_init(sh.sync, kSoftWarps);
+    mbar_init(sh.fin, 1);
+    *sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc(sh.tmem, kTmemCols);
+  griddep_launch_dependents();
+  griddep_wait();
+  if (warp == 0) {
+    // this CTA's share of the blocks, and the unit it begins in
+    long long W = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      long long w = b0 + lane < p.B ? tree_work(p, tree_seq(p, b0 + lane, blockIdx.x == 0)) : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      W += w;
+    }
+    const long long w0 = tree_range(W, blockIdx.x, p.ctas), w1 = tree_range(W, blockIdx.x + 1, p.ctas);
+    long long before = 0;
+    int at_b = 0, at_u = 0, at_j = 0;
+    for (int b0 = 0; b0 < p.B && w1 > w0; b0 += 32) {
+      const bool have = b0 + lane < p.B;
+      const TreeSeq s = have ? tree_seq(p, b0 + lane) : TreeSeq{0, 0, 0};
+      const long long w = have ? tree_work(p, s) : 0;
+      long long sum = w;                                      // inclusive prefix
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += t;
+      }
+      const bool mine = w > 0 && before + sum - w <= w0 && w0 < before + sum;
+      if (mine) {
+        const int in = static_cast<int>(w0 - (before + sum - w)), nblk = tree_blocks(s.n);
+        at_b = b0 + lane;
+        at_u = in / nblk;
+        at_j = in - at_u * nblk;
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, mine);
+      if (m) {
+        const int src = __ffs(m) - 1;
+        at_b = __shfl_sync(0xffffffffu, at_b, src);
+        at_u = __shfl_sync(0xffffffffu, at_u, src);
+        at_j = __shfl_sync(0xffffffffu, at_j, src);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) {
+      sh.sched[0] = at_b;
+      sh.sched[1] = at_u;
+      sh.sched[2] = at_j;
+      sh.sched[3] = static_cast<int>(w1 - w0);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = *sh.tmem;
+  Walk walk(p, sh.sched);
+  Seg sg;
+  int J = 0;                                                  // blocks of the CTA so far
+
+  if (warp == kProdWarp) {
+    // ------------------------------------------------------------ producer
+    bool run = true;
+    int gc = 0;                                               // half blocks issued (raw ring)
+    while (run && walk.next(p, sg)) {
+      const int npg = (sg.n + kBS - 1) / kBS;
+      for (int j = sg.j0; j < sg.j1 && run; ++j, ++J) {
+        // the block's table entries, read before the waits so that their latency overlaps them
+        const int k = j * kPPB + lane;
+        const bool mine = lane < kPPB && k < npg;
+        const int blk = mine ? p.tables[static_cast<long>(sg.b) * p.max_blocks + k] : -1;
+        const bool valid = mine && blk >= 0 && blk < p.NB;
+        if (mine && !valid) record_fault(p.fault, KVQ_FAULT_BLOCK);
+        const unsigned vm = __ballot_sync(0xffffffffu, valid);
+        if constexpr (DIRECT) {
+          const int kb = J % NB;
+          bool ok = true;
+          if (lane == 0 && J >= NB)
+            ok = wait(&sh.k_free[kb], ((J / NB) - 1) & 1, sh.abort) && wait(&sh.v_free[kb], ((J / NB) - 1) & 1, sh.abort);
+          run = __all_sync(0xffffffffu, ok);
+          if (!run) break;
+          if (lane < kPPB) sh.page_ok[kb * kPPB + lane] = valid;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&sh.tile_full[kb], __popc(vm) * Y::REC);
+          __syncwarp();
+          if (valid) {
+            // 16 K rows and 16 V rows of 256 bytes, as two 128-byte halves each
+            const int y = (blk * p.H + sg.kvh) * (2 * kBS), r0 = lane * kBS * 128;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              tma_load_2d(smem + Y::K_OFF + kb * kTile + hh * 16384 + r0, &rows, &sh.tile_full[kb], 128 * hh, y);
+              tma_load_2d(smem + Y::V_OFF + kb * kTile + hh * 16384 + r0, &rows, &sh.tile_full[kb], 128 * hh, y + kBS);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h, ++gc) {
+            const int grp = gc % Y::RH, round = gc / Y::RH;
+            bool ok = true;
+            if (lane == 0 && round > 0) ok = wait(&sh.raw_empty[grp], (round - 1) & 1, sh.abort);
+            run = __all_sync(0xffffffffu, ok);
+            if (!run) break;
+            const int pp = lane - h * Y::HP;
+            const bool here = pp >= 0 && pp < Y::HP;
+            if (here) sh.page_ok[grp * Y::HP + pp] = valid;
+            __syncwarp();
+            if (lane == 0)
+              mbar_arrive_expect_tx(&sh.raw_full[grp], __popc((vm >> (h * Y::HP)) & ((1u << Y::HP) - 1u)) * Y::REC);
+            __syncwarp();
+            if (here && valid)
+              bulk_load(smem + Y::RAW_OFF + (grp * Y::HP + pp) * Y::REC,
+                        p.pages + (static_cast<long>(blk) * p.H + sg.kvh) * Y::REC, Y::REC, &sh.raw_full[grp]);
+          }
+        }
+      }
+    }
+    if (!run && lane == 0) fail(p, sh.abort);
+    // every copy issued must land before the CTA may exit
+    if (lane == 0) {
+      if constexpr (DIRECT) {
+        for (int i = max(0, J - NB); i < J; ++i)
+          if (!mbar_drain(&sh.tile_full[i % NB], (i / NB) & 1)) record_fault(p.fault, KVQ_FAULT_TIMEOUT);
+      } else {
+        constexpr int RH = Y::RH > 0 ? Y::RH : 1;
+        for (int i = max(0, gc - RH); i < gc; ++i)
+          if (!mbar_drain(&sh.raw_full[i % RH], (i / RH) & 1)) record_fault(p.fault, KVQ_FAULT_TIMEOUT);
+      }
+    }
+  } else if (warp >= kConvWarp0) {
+    // ------------------------------------------------------------ converters
+    // thread (c, rr): 16-byte chunk c of rows rr and rr + 8 of every page; thread ct also looks
+    // after token ct of the block (its scale, its row's zeros)
+    const bool isv = warp >= kConvWarp0 + 4;
+    const int cw = (warp - kConvWarp0) & 3, ct = cw * 32 + lane;
+    const int c = ct & 15, rr = ct >> 4;
+    bool run = true;
+    int gc = 0;
+    while (run && walk.next(p, sg)) {
+      const int first = sg.n - sg.L;                          // first drafted position
+      for (int j = sg.j0; j < sg.j1; ++j, ++J) {
+        const int kb = J % NB, slot = J % kNQ;
+        bool ok = true;
+        if (isv) {
+          if (!DIRECT && J >= NB) ok = wait(&sh.v_free[kb], ((J / NB) - 1) & 1, sh.abort);
+        } else {
+          if (!DIRECT && J >= NB) ok = wait(&sh.k_free[kb], ((J / NB) - 1) & 1, sh.abort);
+          if (ok && J >= kNQ) ok = wait(&sh.kq_free[slot], ((J / kNQ) - 1) & 1, sh.abort);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        const bool tail = j * kTreeBlk + kTreeBlk > first;    // holds drafted positions, or the end
+        int pok = 0;
+        bool nf = false;
+        float scale = 0.f;
+        if constexpr (DIRECT) {
+          if (ok) ok = wait(&sh.tile_full[kb], (J / NB) & 1, sh.abort);
+          run = __all_sync(0xffffffffu, ok);
+          if (!run) break;
+#pragma unroll
+          for (int pp = 0; pp < kPPB; ++pp) pok |= (sh.page_ok[kb * kPPB + pp] ? 1 : 0) << pp;
+          if (isv && (tail || pok != (1 << kPPB) - 1)) {
+            const int pos = j * kTreeBlk + ct;
+            const bool keep = pos < sg.n && ((pok >> (ct / kBS)) & 1);
+            uint8_t* tile = smem + Y::V_OFF + kb * kTile;
+            if (!keep || pos >= first) {
+#pragma unroll 4
+              for (int cc = 0; cc < 16; ++cc) {
+                uint4* a = reinterpret_cast<uint4*>(tile + tile_off(ct, cc));
+                uint4 u = keep ? *a : make_uint4(0, 0, 0, 0);
+                const bool drop = drop_nonfinite<BF>(u);
+                if (!keep || drop) *a = u;
+                nf = nf || drop;
+              }
+            }
+          }
+        } else {
+          uint8_t* tile = smem + (isv ? Y::V_OFF : Y::K_OFF) + kb * kTile + tile_off(rr, c) - rr * 128;
+#pragma unroll 1
+          for (int h = 0; h < 2 && ok; ++h) {
+            const int grp = (gc + h) % (Y::RH > 0 ? Y::RH : 1), round = (gc + h) / (Y::RH > 0 ? Y::RH : 1);
+            ok = wait(&sh.raw_full[grp], round & 1, sh.abort);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            const uint8_t* raw = smem + Y::RAW_OFF + grp * Y::HP * Y::REC;
+            uint2 w[Y::HP][2];
+            int hp = 0;
+#pragma unroll
+            for (int pp = 0; pp < Y::HP; ++pp) {
+              hp |= (sh.page_ok[grp * Y::HP + pp] ? 1 : 0) << pp;
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                w[pp][k] = *reinterpret_cast<const uint2*>(raw + pp * Y::REC + (isv ? Y::OFF_V : 0) + (rr + 8 * k) * Y::ROWB + 8 * c);
+            }
+            if constexpr (PT) {
+              if ((ct >> 6) == h) {
+                const int pp = (ct & 63) >> 4;
+                scale = reinterpret_cast<const float*>(raw + pp * Y::REC + Y::OFF_S)[(isv ? kBS : 0) + (ct & 15)];
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.raw_empty[grp]);
+            pok |= hp << (h * Y::HP);
+            const bool whole = !tail && hp == (1 << Y::HP) - 1;
+#pragma unroll
+            for (int pp = 0; pp < Y::HP; ++pp)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int t = (h * Y::HP + pp) * kBS + rr + 8 * k;
+                uint4 u = CD == KVQ_DTYPE_INT8 ? i8x8_to_f16(w[pp][k]) : e4m3x8_to_f16(w[pp][k]);
+                if (!whole) {
+                  const int pos = j * kTreeBlk + t;
+                  if (!(((hp >> pp) & 1) && pos < sg.n)) u = make_uint4(0, 0, 0, 0);
+                  else if (CD == KVQ_DTYPE_FP8_E4M3 && isv && pos >= first) nf = drop_nonfinite<false>(u) || nf;
+                }
+                *reinterpret_cast<uint4*>(tile + t * 128) = u;
+              }
+          }
+          gc += 2;
+          run = __all_sync(0xffffffffu, ok);
+          if (!run) break;
+          if constexpr (PT) {
+            const int pos = j * kTreeBlk + ct;
+            const bool keep = pos < sg.n && ((pok >> (ct / kBS)) & 1);
+            if (!isv) {
+              sh.ks[slot * kTreeBlk + ct] = keep ? scale : 0.f;
+            } else {
+              if (!keep) scale = 0.f;
+              if (pos >= first && !(fabsf(scale) <= 3.4e38f)) {   // an unusable drafted row
+                scale = 0.f;
+                nf = true;
+              }
+              sh.vs[kb * kTreeBlk + ct] = scale;
+              // V scales are >= 0: their bit patterns order as the values do (a NaN, in the
+              // prefix, above all of them: it must not set the exponent)
+              const unsigned m = __reduce_max_sync(0xffffffffu, scale <= 3.4e38f ? __float_as_uint(scale) : 0u);
+              if (lane == 0) sh.vmax[kb * 4 + cw] = __uint_as_float(m);
+            }
+          }
+        }
+        const bool any_nf = __any_sync(0xffffffffu, nf);
+        if (isv && lane == 0) sh.vnf[kb * 4 + cw] = any_nf;
+        if (!isv && ct == 0) sh.pok[slot] = pok;
+        tc::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (isv) {
+            mbar_arrive(&sh.v_full[kb]);
+          } else {
+            mbar_arrive(&sh.k_full[kb]);
+            mbar_arrive(&sh.kq_full[slot]);
+          }
+        }
+      }
+    }
+    if (!run && lane == 0) fail(p, sh.abort);
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    // per unit: S of its first two blocks, then for each block P V and S two blocks ahead.  The
+    // tensor cores work in order, so S of block j + 2 may overwrite the columns P V of block j
+    // reads, and its completion says that P V of block j is complete too.
+    const uint32_t tiles = smem_u32(smem);
+    constexpr uint32_t idS = tc::idesc_f16(BF, false, kTreeRows, kTreeBlk);
+    constexpr uint32_t idPV = tc::idesc_f16(BF, true, kTreeRows, kD);
+    if (lane == 0) {
+      bool ok = true;
+      int unit = 0;
+      auto scores = [&](int jj) -> bool {
+        const int kb = jj % NB;
+        if (!wait(&sh.k_full[kb], (jj / NB) & 1, sh.abort)) return false;
+        if (DIRECT && !wait(&sh.tile_full[kb], (jj / NB) & 1, sh.abort)) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_ss(tbase + 128 * (jj & 1), tc::desc_kmajor(tiles + Y::Q_OFF, kk),
+                     tc::desc_kmajor(tiles + Y::K_OFF + kb * kTile, kk), idS, kk > 0);
+        tc::commit(&sh.k_free[kb]);
+        tc::commit(&sh.s_full[jj & 1]);
+        return true;
+      };
+      while (ok && walk.next(p, sg)) {
+        const int nj = sg.j1 - sg.j0;
+        ok = wait(sh.q_ready, unit & 1, sh.abort);
+        tc::fence_after_sync();
+        if (ok) ok = scores(J);
+        if (ok && nj > 1) ok = scores(J + 1);
+        for (int i = 0; i < nj && ok; ++i) {
+          const int jj = J + i, kb = jj % NB, st = jj & 1;
+          if (!wait(&sh.v_full[kb], (jj / NB) & 1, sh.abort) || !wait(&sh.p_full[st], (jj >> 1) & 1, sh.abort)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+#pragma unroll
+          for (int pa = 0; pa < (HILO ? 2 : 1); ++pa)
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc::mma_ts(tbase + kTmO + 128 * st, tbase + 128 * st + 16 * kk + 8 * pa,
+                         tc::desc_mnmajor(tiles + Y::V_OFF + kb * kTile, kk), idPV, i > 1 || pa > 0 || kk > 0);
+          tc::commit(&sh.v_free[kb]);
+          if (i == nj - 1) tc::commit(sh.o_full);
+          if (i + 2 < nj) ok = scores(jj + 2);
+        }
+        J += nj;
+        ++unit;
+      }
+      if (!ok) fail(p, sh.abort);
+      // one more commit covers every MMA issued above: TMEM is freed only after it arrives
+      tc::commit(sh.fin);
+      if (!mbar_drain(sh.fin, 0)) record_fault(p.fault, KVQ_FAULT_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int st = warp >> 2, quarter = warp & 3;
+    const int r = 32 * quarter + lane;                        // row of the tile (TMEM lane)
+    const uint32_t lanes = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t sbase = lanes + 128 * st, obase = lanes + kTmO + 128 * st;
+    float* ex = reinterpret_cast<float*>(smem + Y::Q_OFF);    // [2][2][128] at a unit's end
+    int* exf = reinterpret_cast<int*>(ex + 512);              // [2] nonfinite drafted rows seen
+    int unit = 0, syncs = 0;
+    bool ok = true;
+    auto sync8 = [&]() -> bool {                              // the eight softmax warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sh.sync);
+      const bool fine = wait(sh.sync, syncs & 1, sh.abort);
+      ++syncs;
+      return __all_sync(0xffffffffu, fine);
+    };
+    while (ok && walk.next(p, sg)) {
+      const int R = sg.L * p.g - sg.tile * kTreeRows;         // rows of the tile that exist
+      // --- q rows -> the Q tile (16 rows per warp, 16 lanes per row)
+      float qsc = p.scale_log2;
+      {
+        if (p.mode == KVQ_SCALE_PER_HEAD) qsc *= p.k_static[sg.kvh];
+        if (p.mode == KVQ_SCALE_PER_TENSOR) qsc *= p.k_static[0];
+        const int c = lane & 15;
+        uint4 u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rq = warp * 16 + 2 * i + (lane >> 4);
+          u[i] = make_uint4(0, 0, 0, 0);
+          if (rq < R) {
+            const int x = sg.tile * kTreeRows + rq, tok = x / p.g;
+            const long row = (static_cast<long>(sg.q0) + tok) * p.Hq + static_cast<long>(sg.kvh) * p.g + (x - tok * p.g);
+            u[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * kD)[c];
+          }
+        }
+        if constexpr (!BF) {
+          if (!p.act_fp16) {
+            // bf16 activations in fp16 tiles: the tile's largest |q| sets a power of two that
+            // keeps every value in range (exact: bf16 has fewer bits than fp16)
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x[8];
+              unpack8<__nv_bfloat16>(u[i], x);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (lane == 0) sh.amax[warp] = amax;
+            ok = sync8();
+            if (!ok) break;
+            amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < kSoftWarps; ++i) amax = fmaxf(amax, sh.amax[i]);
+            int eq = 0;
+            if (amax > 0.f && amax <= 3.4e38f) eq = ilogbf(amax) - 13;
+            const float down = ldexpf(1.f, -eq);
+            qsc = ldexpf(qsc, eq);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x[8];
+              unpack8<__nv_bfloat16>(u[i], x);
+              u[i] = make_uint4(pack_f16x2(x[0] * down, x[1] * down), pack_f16x2(x[2] * down, x[3] * down),
+                                pack_f16x2(x[4] * down, x[5] * down), pack_f16x2(x[6] * down, x[7] * down));
+            }
+          }
+        }
+        if (qsc < 0.f) {                                      // a negative static scale: in q's sign
+          qsc = -qsc;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) (&u[i].x)[e] ^= 0x80008000u;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(smem + Y::Q_OFF + tile_off(warp * 16 + 2 * i + (lane >> 4), c)) = u[i];
+        tc::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sh.q_ready);
+      }
+      const int x = sg.tile * kTreeRows + r;
+      const bool row_ok = r < R, warp_ok = 32 * quarter < R;
+      const int tok = row_ok ? x / p.g : 0;
+      const uint32_t* mrow = p.mask + (static_cast<long>(sg.q0) + tok) * p.mask_words;
+      const int first = sg.n - sg.L;
+      // running maximum m (re-based when a score exceeds it by 2^8) and the exponent ev of the
+      // largest V scale so far: P holds e = 2^(x - m - ev) times the token's V scale, below 2^10;
+      // l and O accumulate in that domain
+      float m = -INFINITY, l = 0.f;
+      int ev = INT_MIN, nfseen = 0;
+      bool begun = false;
+      for (int j = sg.j0; j < sg.j1; ++j) {
+        const int jj = J + j - sg.j0;
+        if ((jj & 1) != st) continue;
+        const int kb = jj % NB, slot = jj % kNQ;
+        ok = wait(&sh.s_full[st], (jj >> 1) & 1, sh.abort) && wait(&sh.kq_full[slot], (jj / kNQ) & 1, sh.abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const int pok = sh.pok[slot];
+        const bool fast = j * kTreeBlk + kTreeBlk <= first && pok == (1 << kPPB) - 1;   // uniform
+        if (warp_ok) {
+          const float* ks = sh.ks + slot * kTreeBlk;
+          const float* vsp = sh.vs + kb * kTreeBlk;
+          uint32_t ra[16], rb[16];
+          float m0 = -INFINITY, m1 = -INFINITY;
+          // --- pass 1: the largest score (times its K scale) of the row, 16 columns at a time
+          auto max16 = [&](const uint32_t* s16, int c0) {
+            if constexpr (PT) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(ks + c0 + i);
+                const float2 a = __fmul2_rn(make_float2(__uint_as_float(s16[i]), __uint_as_float(s16[i + 1])), make_float2(f.x, f.y));
+                const float2 b = __fmul2_rn(make_float2(__uint_as_float(s16[i + 2]), __uint_as_float(s16[i + 3])), make_float2(f.z, f.w));
+                m0 = max3(m0, a.x, a.y);
+                m1 = max3(m1, b.x, b.y);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                m0 = max3(m0, __uint_as_float(s16[i]), __uint_as_float(s16[i + 1]));
+                m1 = max3(m1, __uint_as_float(s16[i + 2]), __uint_as_float(s16[i + 3]));
+              }
+            }
+          };
+          if (fast) {
+            tc::ld16_issue(sbase, ra);
+#pragma unroll
+            for (int cc = 0; cc < 8; cc += 2) {
+              tc::ld_wait16(ra);
+              tc::ld16_issue(sbase + 16 * cc + 16, rb);
+              max16(ra, 16 * cc);
+              tc::ld_wait16(rb);
+              if (cc < 6) tc::ld16_issue(sbase + 16 * cc + 32, ra);
+              max16(rb, 16 * cc + 16);
+            }
+          } else {
+#pragma unroll 1
+            for (int cc = 0; cc < 8; ++cc) {
+              const uint32_t vis = column_bits(mrow, pok, j, cc >> 1, sg.n, sg.L) >> (16 * (cc & 1));
+              tc::ld16(sbase + 16 * cc, ra);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float a = __uint_as_float(ra[i]);
+                if constexpr (PT) a *= ks[16 * cc + i];
+                if ((vis >> i) & 1u) m0 = fmaxf(m0, a);
+              }
+            }
+          }
+          tc::ld16_issue(sbase, ra);                          // pass 2's first columns
+          const float mx = fmaxf(m0, m1) * qsc;
+          float fo = 1.f;
+          if constexpr (PT) {
+            ok = wait(&sh.v_full[kb], (jj / NB) & 1, sh.abort);
+            const float vmx = fmaxf(fmaxf(sh.vmax[kb * 4], sh.vmax[kb * 4 + 1]), fmaxf(sh.vmax[kb * 4 + 2], sh.vmax[kb * 4 + 3]));
+            if (vmx > 0.f) {
+              const int e = max(exponent_of(vmx), -100);
+              if (e > ev) {
+                if (ev != INT_MIN) fo = pow2i(ev - e);
+                ev = e;
+              }
+            }
+          } else if (!fast) {
+            ok = wait(&sh.v_full[kb], (jj / NB) & 1, sh.abort);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!fast) nfseen |= sh.vnf[kb * 4] | sh.vnf[kb * 4 + 1] | sh.vnf[kb * 4 + 2] | sh.vnf[kb * 4 + 3];
+          if (mx > m + kRebase) {
+            fo *= m == -INFINITY ? 0.f : ex2(m - mx);
+            m = mx;
+          }
+          l *= fo;
+          if (begun && __any_sync(0xffffffffu, fo != 1.f)) {
+            // P V of this stream's block before is complete (its S was issued behind it)
+#pragma unroll 1
+            for (int cc = 0; cc < 8; ++cc) {
+              tc::ld16(obase + 16 * cc, rb);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) rb[i] = __float_as_uint(__uint_as_float(rb[i]) * fo);
+              st16(obase + 16 * cc, rb);
+            }
+          }
+          const float off = (m == -INFINITY ? 0.f : m) + (ev == INT_MIN ? 0.f : static_cast<float>(ev));
+          // --- pass 2: e = 2^(x - off), its sum, and P over the scores it came from
+          const float2 noff = make_float2(-off, -off), q2 = make_float2(qsc, qsc);
+          float2 lsum = make_float2(0.f, 0.f);
+          auto p16 = [&](const uint32_t* s16, int c0, auto masked, uint32_t vis) {
+            uint32_t ph[8], pl[8];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              float2 a = make_float2(__uint_as_float(s16[2 * i]), __uint_as_float(s16[2 * i + 1]));
+              float2 b = make_float2(__uint_as_float(s16[2 * i + 2]), __uint_as_float(s16[2 * i + 3]));
+              if constexpr (PT) {
+                const float4 f = *reinterpret_cast<const float4*>(ks + c0 + 2 * i);
+                a = __fmul2_rn(a, make_float2(f.x, f.y));
+                b = __fmul2_rn(b, make_float2(f.z, f.w));
+              }
+              a = __ffma2_rn(a, q2, noff);
+              b = __ffma2_rn(b, q2, noff);
+              if constexpr (decltype(masked)::value) {
+                if (!((vis >> (2 * i)) & 1u)) a.x = -INFINITY;
+                if (!((vis >> (2 * i + 1)) & 1u)) a.y = -INFINITY;
+                if (!((vis >> (2 * i + 2)) & 1u)) b.x = -INFINITY;
+                if (!((vis >> (2 * i + 3)) & 1u)) b.y = -INFINITY;
+              }
+              a = make_float2(ex2(a.x), ex2(a.y));
+              b = make_float2(ex2(b.x), ex2(b.y));
+              lsum = __fadd2_rn(lsum, __fadd2_rn(a, b));
+              if constexpr (PT) {
+                const float4 f = *reinterpret_cast<const float4*>(vsp + c0 + 2 * i);
+                a = __fmul2_rn(a, make_float2(f.x, f.y));
+                b = __fmul2_rn(b, make_float2(f.z, f.w));
+              }
+              if constexpr (HILO) {
+                split2<BF>(a, ph[i], pl[i]);
+                split2<BF>(b, ph[i + 1], pl[i + 1]);
+              } else {
+                ph[i] = pack2<BF>(a);
+                ph[i + 1] = pack2<BF>(b);
+              }
+            }
+            st8(sbase + c0, ph);
+            if constexpr (HILO) st8(sbase + c0 + 8, pl);
+          };
+          if (fast) {
+#pragma unroll
+            for (int cc = 0; cc < 8; cc += 2) {
+              tc::ld_wait16(ra);
+              tc::ld16_issue(sbase + 16 * cc + 16, rb);
+              p16(ra, 16 * cc, std::false_type{}, 0u);
+              tc::ld_wait16(rb);
+              if (cc < 6) tc::ld16_issue(sbase + 16 * cc + 32, ra);
+              p16(rb, 16 * cc + 16, std::false_type{}, 0u);
+            }
+          } else {
+            tc::ld_wait16(ra);
+#pragma unroll 1
+            for (int cc = 0; cc < 8; ++cc) {
+              const uint32_t vis = column_bits(mrow, pok, j, cc >> 1, sg.n, sg.L) >> (16 * (cc & 1));
+              if (cc > 0) tc::ld16(sbase + 16 * cc, ra);
+              p16(ra, 16 * cc, std::true_type{}, vis);
+            }
+          }
+          l += lsum.x + lsum.y;
+          tc::st_wait();
+        }
+        begun = true;
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.p_full[st]);
+          mbar_arrive(&sh.kq_free[slot]);
+        }
+        if (!ok) break;
+      }
+      J += sg.j1 - sg.j0;
+      if (!ok) break;
+      // --- the unit's end: both streams' (offset, sum) through shared memory (the Q tile is
+      // free: every MMA of the unit is complete), then stream st joins the two accumulators
+      // for output channels [64 st, 64 st + 64)
+      ok = __all_sync(0xffffffffu, wait(sh.o_full, unit & 1, sh.abort));
+      ++unit;
+      if (!ok) break;
+      tc::fence_after_sync();
+      ex[(2 * st) * 128 + r] = (m == -INFINITY ? 0.f : m) + (ev == INT_MIN ? 0.f : static_cast<float>(ev));
+      ex[(2 * st + 1) * 128 + r] = l;
+      if (threadIdx.x < 2) exf[threadIdx.x] = 0;
+      ok = sync8();
+      if (!ok) break;
+      if (nfseen && lane == 0) atomicOr(&exf[0], 1);
+      const float o0 = ex[r], l0 = ex[128 + r], o1 = ex[256 + r], l1 = ex[384 + r];
+      ok = sync8();
+      if (!ok) break;
+      const bool nonfinite = exf[0] != 0;
+      // a stream whose sum is 0 saw nothing (or had no block: its accumulator is unwritten)
+      const bool has0 = l0 != 0.f, has1 = l1 != 0.f;
+      const float off = has0 && has1 ? fmaxf(o0, o1) : has0 ? o0 : has1 ? o1 : -INFINITY;
+      const float w0 = has0 ? ex2(o0 - off) : 0.f, w1 = has1 ? ex2(o1 - off) : 0.f;
+      const float lt = (has0 ? l0 * w0 : 0.f) + (has1 ? l1 * w1 : 0.f);
+      const bool whole = sg.j0 == 0 && sg.j1 == sg.nblk;
+      float vmul = 1.f;
+      if (p.mode == KVQ_SCALE_PER_HEAD) vmul = p.v_static[sg.kvh];
+      if (p.mode == KVQ_SCALE_PER_TENSOR) vmul = p.v_static[0];
+      const float mul = whole ? (lt != 0.f ? vmul / lt : 0.f) : vmul;
+      const long prow = (2L * blockIdx.x + (sg.j0 == 0 ? 1 : 0)) * kTreeRows + r;    // partial row
+      const long orow = (static_cast<long>(sg.q0) + tok) * p.Hq + static_cast<long>(sg.kvh) * p.g + (x - tok * p.g);
+      if (!whole && st == 0 && row_ok) *reinterpret_cast<float2*>(p.ws_ml + 2 * prow) = make_float2(off, lt);
+      if (warp_ok) {
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          const int d0 = 64 * st + 16 * cc;
+          uint32_t a[16], b[16];
+          tc::ld16_issue(lanes + kTmO + d0, a);
+          tc::ld16_issue(lanes + kTmO + 128 + d0, b);
+          tc::ld_wait16(a);
+          tc::ld_wait16(b);
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            v[i] = ((has0 ? __uint_as_float(a[i]) * w0 : 0.f) + (has1 ? __uint_as_float(b[i]) * w1 : 0.f)) * mul;
+          if (nonfinite && row_ok) {
+            // drafted rows with infinities or NaN in V: their other elements were in the tile; these
+            // are added to the rows that see them
+            for (int pos = max(first, sg.j0 * kTreeBlk); pos < min(sg.n, sg.j1 * kTreeBlk); ++pos) {
+              const int t = pos - first;
+              if (!((mrow[t >> 5] >> (t & 31)) & 1u)) continue;
+              const int blk = p.tables[static_cast<long>(sg.b) * p.max_blocks + pos / kBS];
+              if (blk < 0 || blk >= p.NB) continue;
+              const uint8_t* rec = p.pages + (static_cast<long>(blk) * p.H + sg.kvh) * Y::REC;
+              const uint8_t* row = rec + Y::OFF_V + (pos % kBS) * Y::ROWB;
+              float s = 1.f;
+              if constexpr (PT) s = reinterpret_cast<const float*>(rec + Y::OFF_S)[kBS + pos % kBS];
+              for (int i = 0; i < 16; ++i) {
+                float e;
+                if constexpr (CD == KVQ_DTYPE_INT8) e = static_cast<float>(static_cast<int8_t>(row[d0 + i]));
+                else if constexpr (CD == KVQ_DTYPE_FP8_E4M3) e = e4m3_to_float(row[d0 + i]);
+                else if constexpr (CD == KVQ_DTYPE_BF16) e = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d0 + i]);
+                else e = __half2float(reinterpret_cast<const __half*>(row)[d0 + i]);
+                e *= s;
+                if (!(fabsf(e) <= 3.4028235e38f)) v[i] += e;
+              }
+            }
+          }
+          if (!row_ok) continue;
+          if (!whole) {
+            float4* dst = reinterpret_cast<float4*>(p.ws_o + prow * kD + d0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else if (p.out_dtype == KVQ_DTYPE_FP32) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * kD + d0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
+            const bool bf = p.out_dtype == KVQ_DTYPE_BF16;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * kD + d0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x0 = v[8 * i + 2 * e], x1 = v[8 * i + 2 * e + 1];
+                w[e] = bf ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
+              }
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+      tc::fence_before_sync();
+      // every warp has read the accumulators and the exchange area before the next unit's Q
+      ok = sync8();
+    }
+    if (!ok && lane == 0) fail(p, sh.abort);
+  }
+  // ---------------------------------------------------------------- teardown
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tbase, kTmemCols);
+  }
+}
+
+// Joins the partial results of units cut between CTAs: one warp per query row, 4 channels
+// per lane.  A unit that lies in one CTA's range was written by that CTA.
+__global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p) {
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);          // (token, head) of the sequence
+  // the schedule depends on the call's inputs only, which this call does not write; they are
+  // read after the wait all the same, since an earlier kernel of the stream may have
+  griddep_wait();
+  const TreeSeq s = tree_seq(p, b);
+  if (i >= s.L * p.Hq) return;
+  long long W = 0, before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int bb = b0 + lane;
+    long long w = bb < p.B ? tree_work(p, tree_seq(p, bb)) : 0, q = bb < b ? w : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      w += __shfl_xor_sync(0xffffffffu, w, o);
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+    }
+    W += w;
+    before += q;
+  }
+  const int tok = i / p.Hq, hq = i - tok * p.Hq, kvh = hq / p.g;
+  const int x = tok * p.g + hq - kvh * p.g, tile = x / kTreeRows, r = x - tile * kTreeRows;
+  const int nblk = tree_blocks(s.n);
+  const long long U0 = before + (static_cast<long long>(kvh) * tree_tiles(p, s.L) + tile) * nblk, U1 = U0 + nblk;
+  // CTA c covers [W c / C, W (c + 1) / C): the last that starts at or before U0, and the last
+  // that starts before U1
+  const int c0 = static_cast<int>(((U0 + 1) * p.ctas + W - 1) / W) - 1, c1 = static_cast<int>((U1 * p.ctas + W - 1) / W) - 1;
+  if (c0 == c1) return;
+  float M = -INFINITY;
+  for (int c = c0; c <= c1; ++c) {
+    if (tree_range(W, c, p.ctas) == tree_range(W, c + 1, p.ctas)) continue;     // an empty range
+    const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * ((2L * c + (c == c0 ? 1 : 0)) * kTreeRows + r));
+    if (v.y != 0.f) M = fmaxf(M, v.x);
+  }
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; ++c) {
+    if (tree_range(W, c, p.ctas) == tree_range(W, c + 1, p.ctas)) continue;
+    const long row = (2L * c + (c == c0 ? 1 : 0)) * kTreeRows + r;
+    const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * row);
+    if (v.y == 0.f) continue;
+    const float w = ex2(v.x - M);
+    const float4 o = *reinterpret_cast<const float4*>(p.ws_o + row * kD + 4 * lane);
+    L = fmaf(v.y, w, L);
+    acc.x = fmaf(o.x, w, acc.x);
+    acc.y = fmaf(o.y, w, acc.y);
+    acc.z = fmaf(o.z, w, acc.z);
+    acc.w = fmaf(o.w, w, acc.w);
+  }
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  const long e0 = (static_cast<long>(s.q0) * p.Hq + i) * kD + 4 * lane;
+  if (p.out_dtype == KVQ_DTYPE_FP32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + e0) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  } else {
+    const bool bf = p.out_dtype == KVQ_DTYPE_BF16;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + e0) =
+        bf ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv))
+           : make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
+  }
+}
+
+template <int CD, bool PT, bool HILO>
+cudaError_t launch(const TreeParams& p, const Geometry& g, cudaStream_t s) {
+  using Y = Layout<CD, PT>;
+  if (g.record != Y::REC) return cudaErrorInvalidValue;
+  // (every call: the attribute belongs to the current device's copy of the kernel)
+  cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<CD, PT, HILO>, cudaFuncAttributeMaxDynamicSharedMemorySize, Y::BYTES);
+  if (e != cudaSuccess) return e;
+  CUtensorMap rows = {};
+  if constexpr (Y::DIRECT) {
+    const long nrows = static_cast<long>(g.NB) * g.H * 2 * kBS;
+    if (!make_rows_map(&rows, p.pages, nrows, Y::ROWB, kBS)) return cudaErrorInvalidValue;
+  }
+  tree_tc_kernel<CD, PT, HILO><<<p.ctas, kThreads, Y::BYTES, s>>>(p, rows);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(tree_merge_kernel, dim3((p.max_tree * p.Hq + 7) / 8, p.B), dim3(256), 0, s, p);
+}
+
+}  // namespace
+
+bool tree_tc_supported(const Geometry& g, int group) {
+  return group >= 1 && g.D == kD && g.bs == kBS && !low_bit(g.cache_dtype) && g.scale_mode != KVQ_SCALE_PER_CHANNEL;
+}
+
+cudaError_t launch_tree_tc(const TreeParams& p, const Geometry& g, cudaStream_t s) {
+  const bool pt = g.scale_mode == KVQ_SCALE_PER_TOKEN_HEAD, hilo = p.out_dtype != KVQ_DTYPE_BF16;
+  switch (g.cache_dtype) {
+    case KVQ_DTYPE_INT8:
+      if (pt) return hilo ? launch<KVQ_DTYPE_INT8, true, true>(p, g, s) : launch<KVQ_DTYPE_INT8, true, false>(p, g, s);
+      return hilo ? launch<KVQ_DTYPE_INT8, false, true>(p, g, s) : launch<KVQ_DTYPE_INT8, false, false>(p, g, s);
+    case KVQ_DTYPE_FP8_E4M3:
+      if (pt) return hilo ? launch<KVQ_DTYPE_FP8_E4M3, true, true>(p, g, s) : launch<KVQ_DTYPE_FP8_E4M3, true, false>(p, g, s);
+      return hilo ? launch<KVQ_DTYPE_FP8_E4M3, false, true>(p, g, s) : launch<KVQ_DTYPE_FP8_E4M3, false, false>(p, g, s);
+    case KVQ_DTYPE_FP16: return hilo ? launch<KVQ_DTYPE_FP16, false, true>(p, g, s) : launch<KVQ_DTYPE_FP16, false, false>(p, g, s);
+    case KVQ_DTYPE_BF16: return launch<KVQ_DTYPE_BF16, false, true>(p, g, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvq

@@ -22,12 +22,17 @@ SCALE = {"none": 0, "per_token_head": 1, "per_head": 2, "per_tensor": 3, "kivi":
          "per_channel": 5, "int4_per_token": 6, "kivi_float_zero": 7}
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARG", 2: "KVQ_ERR_UNSUPPORTED", 3: "KVQ_ERR_CUDA",
           4: "KVQ_ERR_DEVICE_FAULT"}
-FAULT_BITS = {"slot": 1, "block": 2, "context": 4, "seq": 8, "int4_run": 16, "timeout": 32}
+FAULT_BITS = {"slot": 1, "block": 2, "context": 4, "seq": 8, "int4_run": 16, "timeout": 32,
+              "tree": 64}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "wavelength": 3, "yarn": 4}
 EXPORTS = ("kvq_status_string", "kvq_version", "kvq_cache_layout", "kvq_write",
            "kvq_decode_workspace_size", "kvq_decode_attention", "kvq_dequant",
            "kvq_calibrate_fp8_scales", "kvq_read_device_fault", "kvq_decode_attention_noalloc",
            "kvq_append_decode_attention", "kvq_calibrate_channel_scales", "kvq_flush_ring",
-           "kvq_prefill_attention", "kvq_decode_plan", "kvq_calibrate_head_scales")
+           "kvq_prefill_attention", "kvq_decode_plan", "kvq_calibrate_head_scales",
+           "kvq_rope_frequencies", "kvq_rope", "kvq_rope_write", "kvq_gather",
+           "kvq_tree_workspace_size", "kvq_tree_attention", "kvq_tree_commit")
 
 
 class CacheDesc(ctypes.Structure):
@@ -42,6 +47,13 @@ class CacheDesc(ctypes.Structure):
                 ("fault", ctypes.c_void_p)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_context", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("attention_factor", ctypes.c_double)]
+
+
 class KVQError(RuntimeError):
     def __init__(self, status, what):
         super().__init__("%s failed: %s" % (what, STATUS.get(status, status)))
@@ -54,7 +66,7 @@ def _load():
                           "`python -m quantized_paged_kv_02_b200.build`" % LIB_PATH)
     lib = ctypes.CDLL(LIB_PATH)
     P, I, Z, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
-    D = ctypes.POINTER(CacheDesc)
+    D, R, L = ctypes.POINTER(CacheDesc), ctypes.POINTER(RopeDesc), ctypes.c_int64
     sig = {
         "kvq_status_string": (ctypes.c_char_p, [I]),
         "kvq_version": (I, []),
@@ -74,6 +86,13 @@ def _load():
         "kvq_calibrate_head_scales": (I, [P, I, I, I, ctypes.c_int32, F, P, P]),
         "kvq_flush_ring": (I, [D, P, P, P, I, P]),
         "kvq_prefill_attention": (I, [D, P, I, I, I, P, I, P, I, P, I, F, P, ctypes.c_int32, P]),
+        "kvq_rope_frequencies": (I, [R, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
+        "kvq_rope": (I, [R, P, ctypes.c_int32, I, P, I, P, L, I, P, L, P, L, I, P, L, P]),
+        "kvq_rope_write": (I, [D, R, P, P, I, P, L, I, P, L, P, L, P, L, P, P]),
+        "kvq_gather": (I, [D, P, I, P, P, P]),
+        "kvq_tree_workspace_size": (I, [D, I, I, I, I, ctypes.POINTER(Z)]),
+        "kvq_tree_attention": (I, [D, P, I, I, I, P, I, P, I, P, I, P, I, F, P, ctypes.c_int32, P, Z, P]),
+        "kvq_tree_commit": (I, [D, P, I, P, I, P, P, I, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -257,14 +276,183 @@ def kvq_read_device_fault(desc, reset=True, stream=None):
     return int(out[0]), int(out[1])
 
 
+def _rows(t, heads, dim, what):
+    """Token stride of a [T][heads][dim] tensor whose rows are dense (a view into fused
+    projection rows is fine)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError("%s must be [tokens, %d, %d], got %s" % (what, heads, dim, tuple(t.shape)))
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError("%s: the heads of a token must be contiguous" % what)
+    # (the stride of a single token, or of a one-token view, says nothing)
+    return max(t.stride(0), heads * dim) if t.shape[0] > 1 else heads * dim
+
+
+def _like(t, ref, what):
+    """t has the type and device of ref."""
+    if t.dtype != ref.dtype or t.device != ref.device:
+        raise TypeError("%s must be %s on %s, got %s on %s" % (what, ref.dtype, ref.device, t.dtype, t.device))
+    return t
+
+
+def _count(t, n, what):
+    """Index tensor of n entries (contiguous int32)."""
+    if t.numel() != n:
+        raise ValueError("%s must have %d entries, got %d" % (what, n, t.numel()))
+    return _i32(t)
+
+
+def kvq_rope_frequencies(rope):
+    """(frequencies in radians per position, factor of cosine and sine) of a RopeDesc."""
+    f = (ctypes.c_double * max(rope.rot_dim // 2, 1))()
+    m = ctypes.c_double(0.0)
+    _check(lib.kvq_rope_frequencies(ctypes.byref(rope), f, ctypes.byref(m)), "kvq_rope_frequencies")
+    return list(f)[:rope.rot_dim // 2], m.value
+
+
+def kvq_rope(rope, freqs, positions, q=None, k=None, q_out=None, k_out=None, stream=None):
+    """Rotate q [T, Hq, D] and / or k [T, H, D] (token strides as they are) into q_out / k_out
+    (given, or allocated dense); an output may be its input."""
+    ref = q if q is not None else k
+    T, D = ref.shape[0], ref.shape[2]
+    args = []
+    outs = []
+    for x, out, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            args += [None, 0, 0, None, 0]
+            outs.append(None)
+            continue
+        if x.shape[0] != T:
+            raise ValueError("q and k must have the same number of tokens")
+        xs = _rows(_like(x, ref, what), x.shape[1], D, what)
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        elif out.shape != x.shape:
+            raise ValueError("%s_out must have the shape of %s" % (what, what))
+        args += [_ptr(x), xs, int(x.shape[1]), _ptr(out), _rows(_like(out, x, what + "_out"), x.shape[1], D, what + "_out")]
+        outs.append(out)
+    _check(lib.kvq_rope(ctypes.byref(rope), _ptr(freqs), DTYPE[_act(ref)], D, _ptr(_count(positions, T, "positions")), T,
+                        *args, _stream(stream)), "kvq_rope")
+    return tuple(outs)
+
+
+def kvq_rope_write(desc, rope, freqs, positions, q, k_new, v_new, slot_mapping, q_out=None, stream=None):
+    """kvq_rope of q and k_new, then kvq_write of the rotated keys and of v_new, in one launch.
+    Returns q_out (None without q)."""
+    T, H, D = k_new.shape[0], desc.num_kv_heads, desc.head_dim
+    if DTYPE[_act(k_new)] != desc.act_dtype:
+        raise TypeError("k_new must have the cache's activation type")
+    ks = _rows(k_new, H, D, "k_new")
+    vs = _rows(_like(v_new, k_new, "v_new"), H, D, "v_new")
+    if v_new.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("q, k_new and v_new must have the same number of tokens")
+    qa = [None, 0, 0, None, 0]
+    if q is not None:
+        hq = int(q.shape[1])
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        qa = [_ptr(q), _rows(_like(q, k_new, "q"), hq, D, "q"), hq, _ptr(q_out),
+              _rows(_like(q_out, k_new, "q_out"), hq, D, "q_out")]
+    _check(lib.kvq_rope_write(ctypes.byref(desc), ctypes.byref(rope), _ptr(freqs),
+                              _ptr(_count(positions, T, "positions")), T, *qa, _ptr(k_new), ks, _ptr(v_new), vs,
+                              _ptr(_count(slot_mapping, T, "slot_mapping")), _stream(stream)), "kvq_rope_write")
+    return q_out
+
+
+def kvq_gather(desc, slots, k_out, v_out, stream=None):
+    """K and V rows of the listed cache slots, dequantized to the activation type."""
+    n = int(slots.numel())
+    for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+        if tuple(t.shape) != (n, desc.num_kv_heads, desc.head_dim) or not t.is_contiguous():
+            raise ValueError("%s must be contiguous [%d, %d, %d]" % (what, n, desc.num_kv_heads, desc.head_dim))
+        if DTYPE[_act(t)] != desc.act_dtype:
+            raise TypeError("%s must have the cache's activation type" % what)
+    _check(lib.kvq_gather(ctypes.byref(desc), _ptr(_i32(slots)), n, _ptr(k_out), _ptr(v_out), _stream(stream)),
+           "kvq_gather")
+    return k_out, v_out
+
+
+def kvq_tree_workspace_size(desc, batch, num_q_heads, max_tree, max_context):
+    n = ctypes.c_size_t(0)
+    _check(lib.kvq_tree_workspace_size(ctypes.byref(desc), batch, num_q_heads, max_tree, max_context,
+                                       ctypes.byref(n)), "kvq_tree_workspace_size")
+    return n.value
+
+
+def kvq_tree_attention(desc, q, q_start, max_tree, tree_mask, block_tables, context_lens, max_context, out,
+                       workspace=None, softmax_scale=0.0, stream=None):
+    """Attention of each sequence's drafted tokens (rows q_start[b] .. q_start[b+1]-1 of q, the newest
+    cached positions) over the cached prefix and the drafted tokens its mask row names.  tree_mask:
+    int32 [tokens, words], the bits of the C ABI's uint32."""
+    T, Hq, D = q.shape
+    if D != desc.head_dim or DTYPE[_act(q)] != desc.act_dtype or not q.is_contiguous():
+        raise ValueError("q must be contiguous [tokens, heads, %d] of the cache's activation type" % desc.head_dim)
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous and have the shape of q")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+        raise ValueError("tree_mask must be [tokens, words]")
+    B = int(q_start.numel()) - 1
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [%d, blocks]" % B)
+    out_dt = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}[out.dtype]
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.kvq_tree_attention(
+        ctypes.byref(desc), _ptr(q), T, B, Hq, _ptr(_i32(q_start)), int(max_tree), _ptr(_i32(tree_mask)),
+        int(tree_mask.shape[1]), _ptr(_i32(block_tables)), int(block_tables.shape[1]),
+        _ptr(_count(context_lens, B, "context_lens")), int(max_context), float(softmax_scale), _ptr(out), DTYPE[out_dt],
+        _ptr(workspace), ws_bytes, _stream(stream)), "kvq_tree_attention")
+    return out
+
+
+def kvq_tree_commit(desc, path, accepted, q_start, block_tables, context_lens, new_lens=None, stream=None):
+    """Move the cache rows of each sequence's accepted path (drafted indexes path[b, :accepted[b]]) to the
+    first drafted positions; new_lens receives the new context lengths."""
+    B = int(accepted.numel())
+    if path.dim() != 2 or path.shape[0] != B or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("path and block_tables must have one row per sequence")
+    _check(lib.kvq_tree_commit(
+        ctypes.byref(desc), _ptr(_i32(path)), int(path.shape[1]), _ptr(_i32(accepted)), B,
+        _ptr(_count(q_start, B + 1, "q_start")), _ptr(_i32(block_tables)), int(block_tables.shape[1]),
+        _ptr(_count(context_lens, B, "context_lens")),
+        None if new_lens is None else _ptr(_count(new_lens, B, "new_lens")), _stream(stream)), "kvq_tree_commit")
+    return new_lens
+
+
 # ----------------------------------------------------------------------------- holder
+class Rope:
+    """A rotary embedding: its descriptor and its frequencies on the device.
+
+    layout "half" or "interleaved"; scaling "none", "linear", "ntk", "wavelength" or "yarn" (include/kvq.h);
+    freqs: frequencies of the caller's own (radians per position), instead of the descriptor's."""
+
+    def __init__(self, head_dim, rot_dim=None, theta=10000.0, layout="half", scaling="none", factor=1.0,
+                 original_context=0, low=1.0, high=4.0, attention_factor=0.0, freqs=None, device="cuda"):
+        r = self.desc = RopeDesc()
+        self.head_dim = head_dim
+        r.layout, r.scaling = ROPE_LAYOUT[layout], ROPE_SCALING[scaling]
+        r.rot_dim = head_dim if rot_dim is None else rot_dim
+        r.original_context, r.theta, r.factor = original_context, theta, factor
+        r.low, r.high, r.attention_factor = low, high, attention_factor
+        own, self.attention_factor = kvq_rope_frequencies(r)
+        f = torch.tensor(own, dtype=torch.float64) if freqs is None else freqs.to(torch.float64)
+        if f.shape != (r.rot_dim // 2,):
+            raise ValueError("freqs must have rot_dim / 2 entries")
+        self.freqs = f.to(device).contiguous()
+
+    def apply(self, positions, q=None, k=None, q_out=None, k_out=None, stream=None):
+        """(rotated q, rotated k); None for one not given."""
+        return kvq_rope(self.desc, self.freqs, positions, q, k, q_out, k_out, stream)
+
+
 class PagedKVCache:
     """One layer's cache, allocated with torch in the layout of include/kvq.h: the page
     records pool, the static scale arrays (PER_HEAD / PER_TENSOR) and the INT4 ring."""
 
     def __init__(self, cache_dtype, act_dtype, scale_mode, num_blocks, block_size, num_kv_heads,
                  head_dim, device="cuda", group_size=64, residual_len=128, residual_cap=192,
-                 max_seqs=0, static_k_scale=None, static_v_scale=None, fill=0x5A, fault=True):
+                 max_seqs=0, static_k_scale=None, static_v_scale=None, fill=0x5A, fault=True,
+                 pages=None):
         self.desc = CacheDesc()
         d = self.desc
         d.cache_dtype, d.act_dtype, d.scale_mode = DTYPE[cache_dtype], DTYPE[act_dtype], SCALE[scale_mode]
@@ -276,7 +464,12 @@ class PagedKVCache:
         self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
         self.device = torch.device(device)
         self.record, pages_b, ss_b, res_b = kvq_cache_layout(d)
-        self.pages = torch.full((pages_b,), fill, dtype=torch.uint8, device=self.device)
+        if pages is None:
+            self.pages = torch.full((pages_b,), fill, dtype=torch.uint8, device=self.device)
+        else:                                     # a pool the caller holds
+            if pages.dtype != torch.uint8 or not pages.is_contiguous() or pages.numel() < pages_b:
+                raise ValueError("pages must be a contiguous uint8 pool of at least %d bytes" % pages_b)
+            self.pages, self.device = pages, pages.device
         self.k_scales = self.v_scales = self.residual = None
         if ss_b:
             n = ss_b // 4
@@ -335,6 +528,40 @@ class PagedKVCache:
             out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
         return kvq_prefill_attention(self.desc, q, q_start, max_q_len, block_tables, context_lens,
                                      max_context, out, softmax_scale, stream)
+
+    def rope_write(self, rope, positions, q, k_new, v_new, slot_mapping, q_out=None, stream=None):
+        """Rotate q and k_new, store the rotated keys and v_new; returns the rotated q."""
+        return kvq_rope_write(self.desc, rope.desc, rope.freqs, positions, q, k_new, v_new, slot_mapping, q_out,
+                              stream)
+
+    def gather(self, slots, k_out=None, v_out=None, stream=None):
+        """(K, V) rows of the listed slots, [rows, H, D] of the activation type."""
+        shape = (int(slots.numel()), self.num_kv_heads, self.head_dim)
+        dt = torch.bfloat16 if self.act_dtype == "bf16" else torch.float16
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dt, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dt, device=self.device)
+        return kvq_gather(self.desc, slots, k_out, v_out, stream)
+
+    def tree_workspace_size(self, batch, num_q_heads, max_tree, max_context):
+        return kvq_tree_workspace_size(self.desc, batch, num_q_heads, max_tree, max_context)
+
+    def tree_attention(self, q, q_start, max_tree, tree_mask, block_tables, context_lens, max_context, out=None,
+                       out_dtype=torch.float32, workspace=None, softmax_scale=0.0, stream=None):
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        if workspace is None:
+            n = self.tree_workspace_size(int(q_start.numel()) - 1, q.shape[1], max_tree, max_context)
+            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device) if n else None
+        return kvq_tree_attention(self.desc, q, q_start, max_tree, tree_mask, block_tables, context_lens,
+                                  max_context, out, workspace, softmax_scale, stream)
+
+    def tree_commit(self, path, accepted, q_start, block_tables, context_lens, new_lens=None, stream=None):
+        """Keep each sequence's accepted path; returns the new context lengths."""
+        if new_lens is None:
+            new_lens = torch.empty_like(context_lens)
+        return kvq_tree_commit(self.desc, path, accepted, q_start, block_tables, context_lens, new_lens, stream)
 
     def flush_ring(self, seq_ids, positions, block_ids, stream=None):
         kvq_flush_ring(self.desc, seq_ids, positions, block_ids, stream)
