@@ -8,7 +8,7 @@ namespace kvq {
 
 constexpr int kTreeMax = 1024;       // drafted tokens per sequence at most
 constexpr int kTreeRows = 128;       // tensor-core kernel: query rows per tile
-constexpr int kTreeBlk = 128;        // ... and cached tokens per block
+constexpr int kTreeBlk = 64;         // ... and cached tokens per block
 
 struct TreePlan {
   int kernel;          // 0 CUDA cores, 1 tensor cores (tcgen05)
@@ -85,7 +85,7 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t* row, int pos, int 
 }
 
 // Block-balanced schedule of the tensor-core kernel.  A unit is one (sequence, kv head, tile of
-// 128 query rows) and has ceil(n / 128) blocks; the blocks of all units, in the order
+// 128 query rows) and has ceil(n / 64) blocks; the blocks of all units, in the order
 // (sequence, kv head, tile), are cut into ctas contiguous ranges.  A CTA has at most two
 // segments that do not hold a whole unit: one that does not begin its unit (partial slot
 // 2 c) and one that begins but does not end it (slot 2 c + 1).

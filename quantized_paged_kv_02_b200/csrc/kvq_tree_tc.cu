@@ -45,11 +45,14 @@ namespace kvq {
 namespace {
 
 constexpr int kD = 128, kBS = 16, kPPB = kTreeBlk / kBS;
-constexpr int kThreads = 576;
-constexpr int kSoftWarps = 8, kProdWarp = 8, kMmaWarp = 9, kConvWarp0 = 10;
-constexpr int kTile = 32768;         // 128 x 128 16-bit elements
-constexpr int kNQ = 4;               // slots of per-block K data
+constexpr int kThreads = 608;
+constexpr int kSoftWarps = 8, kProdWarp = 8, kScoreWarp = 9, kConvWarp0 = 10, kOutWarp = 18;
+constexpr int kTile = 16384;         // K or V of a block: 64 x 128 16-bit elements
+constexpr int kQTile = 32768;        // 128 x 128
+constexpr int kNS = 4;               // score buffers: two per stream
+constexpr int kNQ = 8;               // slots of per-block scales and page flags
 constexpr float kRebase = 8.f;       // log2 headroom before the running maximum is re-based
+// TMEM columns: scores / P of block J in [64 (J % 4), +64), O of stream s in [256 + 128 s, +128)
 constexpr uint32_t kTmemCols = 512, kTmO = 256;
 
 template <int CD, bool PT>
@@ -59,24 +62,28 @@ struct Layout {
   static constexpr int ROWB = DIRECT ? 2 * kD : kD;
   static constexpr int OFF_V = kBS * ROWB, OFF_S = 2 * kBS * ROWB;
   static constexpr int REC = OFF_S + (PT ? 8 * kBS : 0);
-  static constexpr int NB = DIRECT ? 3 : 2;                     // K and V tile buffers each
-  static constexpr int HP = kPPB / 2;                           // pages per half block
-  static constexpr int RH = DIRECT ? 0 : 3;                     // raw ring, in half blocks
+  // K and V tile buffers (a K tile is free once S has read it, a V tile only after P V), and the
+  // raw ring of blocks (8-bit caches)
+  static constexpr int NBK = DIRECT ? 6 : 2, NBV = DIRECT ? 6 : 3;
+  static constexpr int RS = DIRECT ? 0 : 5;
+  static constexpr int RSD = RS > 0 ? RS : 1;                   // (a divisor)
   static constexpr int K_OFF = 0;
-  static constexpr int V_OFF = NB * kTile;
-  static constexpr int Q_OFF = V_OFF + NB * kTile;
-  static constexpr int RAW_OFF = Q_OFF + kTile;
-  static constexpr int KS_OFF = RAW_OFF + RH * HP * REC;        // float [kNQ][128] K scales (PT)
-  static constexpr int VS_OFF = KS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [NB][128]
-  static constexpr int MISC_OFF = VS_OFF + (PT ? NB * kTreeBlk * 4 : 0);
-  // page flags of the raw ring / tile buffers; pok [kNQ]; vmax, nonfinite [NB][4]; amax [8];
-  // schedule [4]; tmem, abort
-  static constexpr int NPOK = DIRECT ? NB * kPPB : RH * HP;
-  static constexpr int WORDS = NPOK + kNQ + 8 * NB + 8 + 6 + 2;
+  static constexpr int V_OFF = NBK * kTile;
+  static constexpr int Q_OFF = V_OFF + NBV * kTile;
+  static constexpr int RAW_OFF = Q_OFF + kQTile;
+  static constexpr int KS_OFF = RAW_OFF + RS * kPPB * REC;      // float [kNQ][64] K scales (PT)
+  static constexpr int VS_OFF = KS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [kNQ][64]: V scales
+  static constexpr int MISC_OFF = VS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);
+  // vmax [kNQ][4]; nonfinite flags of scales [kNQ][4] and of V rows [NBV][4]; page masks of the raw
+  // ring / tile buffers; pok [kNQ]; amax [8]; schedule [6]; tmem, abort
+  static constexpr int NPOK = DIRECT ? NBK : RS;
+  static constexpr int WORDS = 8 * kNQ + 4 * NBV + NPOK + kNQ + 8 + 6 + 2;
   static constexpr int BAR_OFF = (MISC_OFF + 4 * WORDS + 7) / 8 * 8;
-  // raw_full, raw_empty [RH]; tile_full [NB] (DIRECT); k_full, k_free, v_full, v_free [NB];
-  // s_full, p_full [2]; kq_full, kq_free [kNQ]; q_ready, o_full, sync, fin
-  static constexpr int NBARS = 2 * RH + 5 * NB + 4 + 2 * kNQ + 4;
+  static_assert(MISC_OFF % 16 == 0, "vmax is read four at a time");
+  static_assert(!DIRECT || NBK == NBV, "16-bit caches fill K and V of a buffer together");
+  // raw_full, raw_empty [RS]; tile_full [NBK] (DIRECT); k_full, k_free [NBK]; v_full, v_free
+  // [NBV]; s_full, s_free, p_full [kNS]; pv_done [2]; kq_full, kq_free [kNQ]; q_ready, o_full, sync, fin [2]
+  static constexpr int NBARS = 2 * RS + 3 * NBK + 2 * NBV + 3 * kNS + 2 + 2 * kNQ + 5;
   static constexpr int BYTES = 1024 + BAR_OFF + 8 * NBARS;
   static_assert(BYTES <= 227 * 1024, "fits the shared memory of one CTA");
   static_assert(BYTES > 114 * 1024, "one CTA per SM: its TMEM allocation never waits for a peer");
@@ -130,9 +137,9 @@ struct Walk {
 };
 
 struct Shared {
-  uint64_t *raw_full, *raw_empty, *tile_full, *k_full, *k_free, *v_full, *v_free, *s_full, *p_full, *kq_full,
+  uint64_t *raw_full, *raw_empty, *tile_full, *k_full, *k_free, *v_full, *v_free, *s_full, *s_free, *p_full, *pv_done, *kq_full,
       *kq_free, *q_ready, *o_full, *sync, *fin;
-  int *page_ok, *pok, *vnf, *sched;
+  int *pages, *pok, *snf, *vnf, *sched;
   float *vmax, *amax, *ks, *vs;
   uint32_t* tmem;
   volatile int* abort;
@@ -154,15 +161,54 @@ __device__ __forceinline__ void fail(const TreeParams& p, volatile int* abort) {
   *abort = 1;
 }
 
-// Swizzled byte offset of 16-byte chunk c (8 elements, c < 16) of row t in a 128 x 128 tile.
+// Swizzled byte offset of 16-byte chunk c (8 elements, c < 16) of row t in a tile of R rows.
+template <int R>
 __device__ __forceinline__ uint32_t tile_off(int t, int c) {
-  return static_cast<uint32_t>((c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4));
+  return static_cast<uint32_t>((c >> 3) * (R * 128) + t * 128 + (((c & 7) ^ (t & 7)) << 4));
 }
 
+// Descriptors of a tile's first k step.  K-major (rows M or N, contiguous along K): 8-row groups
+// 1024 bytes apart; a step of 16 elements is 32 bytes on, the fifth in the second column half.
+// MN-major (rows K, contiguous along N): column halves R * 128 bytes apart, a step of 16 rows 2048
+// bytes on.  (Descriptors count 16 bytes.)
+__device__ __forceinline__ uint64_t first_kmajor(uint32_t tile) { return tc::smem_desc(tile, 16u, 1024u); }
+template <int R>
+__device__ __forceinline__ uint64_t step_kmajor(int kk) { return (kk >> 2) * (R * 8) + (kk & 3) * 2; }
+__device__ __forceinline__ uint64_t first_mnmajor(uint32_t tile) { return tc::smem_desc(tile, kTreeBlk * 128u, 1024u); }
+
+// One thread of the warp issues (the operands stay in the warp's uniform registers, which a
+// branch on the lane would take them out of).
+__device__ __forceinline__ void mma_ss_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u) : "memory");
+}
+__device__ __forceinline__ void mma_ts_one(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u) : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Eight INT8 codes -> fp16, exactly: byte c + 128 under the exponent of 1024, less 1152.
 __device__ __forceinline__ uint4 i8x8_to_f16(uint2 w) {
   const uint32_t a = w.x ^ 0x80808080u, b = w.y ^ 0x80808080u;
-  return make_uint4(i8x2_to_f16x2(a, kLoPair), i8x2_to_f16x2(a, kHiPair), i8x2_to_f16x2(b, kLoPair),
-                    i8x2_to_f16x2(b, kHiPair));
+  uint4 u = make_uint4(__byte_perm(a, 0x64646464u, kLoPair), __byte_perm(a, 0x64646464u, kHiPair),
+                       __byte_perm(b, 0x64646464u, kLoPair), __byte_perm(b, 0x64646464u, kHiPair));
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __half2& h = *reinterpret_cast<__half2*>(&(&u.x)[i]);
+    h = __hsub2(h, bias);
+  }
+  return u;
 }
 
 __device__ __forceinline__ uint4 e4m3x8_to_f16(uint2 w) {
@@ -198,9 +244,43 @@ __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
-  st8(taddr, r);
-  st8(taddr + 8, r + 8);
+// Bring a page record into L2 (a hint: it completes on its own and faults nothing).
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// O or P columns [base, base + 16 n) of the warp's lanes times a power of two per lane: float32
+// values, or 16-bit pairs (one element's factor in f2).
+__device__ __forceinline__ void scale_f32(uint32_t base, int n, float f) {
+#pragma unroll 1
+  for (int c = 0; c < n; ++c) {
+    uint32_t r[16];
+    tc::ld16(base + 16 * c, r);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+    st8(base + 16 * c, r);
+    st8(base + 16 * c + 8, r + 8);
+  }
+}
+template <bool BF, bool HILO>
+__device__ __forceinline__ void scale_p(uint32_t base, int n, float f) {
+#pragma unroll 1
+  for (int c = 0; c < n; ++c) {
+    uint32_t r[16];
+    tc::ld16(base + 16 * c, r);
+#pragma unroll
+    for (int i = 0; i < (HILO ? 16 : 8); ++i) {
+      if constexpr (BF) {
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r[i]), __float2bfloat162_rn(f));
+        r[i] = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&r[i]), __float2half2_rn(f));
+        r[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    st8(base + 16 * c, r);
+    if constexpr (HILO) st8(base + 16 * c + 8, r + 8);
+  }
 }
 
 // 16-bit pairs of w whose exponent is all ones (infinity, NaN) set to zero; true if any was.
@@ -229,18 +309,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap rows) {
   using Y = Layout<CD, PT>;
   constexpr bool BF = Y::BF, DIRECT = Y::DIRECT;
-  constexpr int NB = Y::NB;
+  constexpr int NBK = Y::NBK, NBV = Y::NBV, kAll = (1 << kPPB) - 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Shared sh;
   {
     int* w = reinterpret_cast<int*>(smem + Y::MISC_OFF);
-    sh.page_ok = w;
-    sh.pok = w + Y::NPOK;
-    sh.vnf = sh.pok + kNQ;                                   // [NB][4]
-    sh.vmax = reinterpret_cast<float*>(sh.vnf + 4 * NB);     // [NB][4]
-    sh.amax = sh.vmax + 4 * NB;                              // [8]
+    sh.vmax = reinterpret_cast<float*>(w);                   // [kNQ][4]
+    sh.snf = w + 4 * kNQ;                                    // [kNQ][4]
+    sh.vnf = sh.snf + 4 * kNQ;                               // [NBV][4]
+    sh.pages = sh.vnf + 4 * NBV;
+    sh.pok = sh.pages + Y::NPOK;
+    sh.amax = reinterpret_cast<float*>(sh.pok + kNQ);        // [8]
     sh.sched = reinterpret_cast<int*>(sh.amax + 8);          // [6]
     sh.tmem = reinterpret_cast<uint32_t*>(sh.sched + 6);
     sh.abort = reinterpret_cast<volatile int*>(sh.sched + 7);
@@ -248,38 +329,44 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     sh.vs = reinterpret_cast<float*>(smem + Y::VS_OFF);
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Y::BAR_OFF);
     auto take = [&](int n) { uint64_t* r = bar; bar += n; return r; };
-    sh.raw_full = take(Y::RH);
-    sh.raw_empty = take(Y::RH);
-    sh.tile_full = take(NB);
-    sh.k_full = take(NB);
-    sh.k_free = take(NB);
-    sh.v_full = take(NB);
-    sh.v_free = take(NB);
-    sh.s_full = take(2);
-    sh.p_full = take(2);
+    sh.raw_full = take(Y::RS);
+    sh.raw_empty = take(Y::RS);
+    sh.tile_full = take(NBK);
+    sh.k_full = take(NBK);
+    sh.k_free = take(NBK);
+    sh.v_full = take(NBV);
+    sh.v_free = take(NBV);
+    sh.s_full = take(kNS);
+    sh.s_free = take(kNS);
+    sh.p_full = take(kNS);
+    sh.pv_done = take(2);
     sh.kq_full = take(kNQ);
     sh.kq_free = take(kNQ);
     sh.q_ready = take(1);
     sh.o_full = take(1);
     sh.sync = take(1);
-    sh.fin = take(1);
+    sh.fin = take(2);
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Y::RH; ++i) {
+    for (int i = 0; i < Y::RS; ++i) {
       mbar_init(&sh.raw_full[i], 1);
       mbar_init(&sh.raw_empty[i], 8);
     }
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < NBK; ++i) {
       mbar_init(&sh.tile_full[i], 1);
       mbar_init(&sh.k_full[i], 4);
       mbar_init(&sh.k_free[i], 1);
+    }
+    for (int i = 0; i < NBV; ++i) {
       mbar_init(&sh.v_full[i], 4);
       mbar_init(&sh.v_free[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kNS; ++i) {
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], 1);
       mbar_init(&sh.p_full[i], 4);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.pv_done[i], 1);
     for (int i = 0; i < kNQ; ++i) {
       mbar_init(&sh.kq_full[i], 4);
       mbar_init(&sh.kq_free[i], 4);
@@ -287,11 +374,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     mbar_init(sh.q_ready, kSoftWarps);
     mbar_init(sh.o_full, 1);
     mbar_init(sh.sync, kSoftWarps);
-    mbar_init(sh.fin, 1);
+    mbar_init(&sh.fin[0], 1);
+    mbar_init(&sh.fin[1], 1);
     *sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) tc::tmem_alloc(sh.tmem, kTmemCols);
+  if (warp == kOutWarp) tc::tmem_alloc(sh.tmem, kTmemCols);
   griddep_launch_dependents();
   griddep_wait();
   if (warp == 0) {
@@ -351,110 +439,106 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
   if (warp == kProdWarp) {
     // ------------------------------------------------------------ producer
     bool run = true;
-    int gc = 0;                                               // half blocks issued (raw ring)
+    int buf = 0, round = 0;                                   // of the raw ring / the tiles
+    constexpr int RING = DIRECT ? NBK : Y::RSD;
     while (run && walk.next(p, sg)) {
       const int npg = (sg.n + kBS - 1) / kBS;
+      // table entries 32 pages (8 blocks) at a time, one per lane, the next 32 loaded while these
+      // are used and their pages sent for into L2 (a block's own entries, read when it is due,
+      // would put a load's latency between every two blocks)
+      const int32_t* table = p.tables + static_cast<long>(sg.b) * p.max_blocks;
+      const int base = sg.j0 * kPPB, stop = min(sg.j1 * kPPB, npg);
+      int cur = -1, next = base + lane < stop ? table[base + lane] : -1;
       for (int j = sg.j0; j < sg.j1 && run; ++j, ++J) {
-        // the block's table entries, read before the waits so that their latency overlaps them
-        const int k = j * kPPB + lane;
-        const bool mine = lane < kPPB && k < npg;
-        const int blk = mine ? p.tables[static_cast<long>(sg.b) * p.max_blocks + k] : -1;
+        const int at = (j - sg.j0) & 7;                       // block of the batch
+        if (at == 0) {
+          cur = next;
+          const int k = j * kPPB + 32 + lane;
+          next = k < stop ? table[k] : -1;
+        } else if (at == 2 && next >= 0 && next < p.NB) {
+          prefetch_l2(p.pages + (static_cast<long>(next) * p.H + sg.kvh) * Y::REC, Y::REC);
+        }
+        const int blk = __shfl_sync(0xffffffffu, cur, at * kPPB + (lane & (kPPB - 1)));
+        const bool mine = lane < kPPB && j * kPPB + lane < stop;
         const bool valid = mine && blk >= 0 && blk < p.NB;
         if (mine && !valid) record_fault(p.fault, KVQ_FAULT_BLOCK);
         const unsigned vm = __ballot_sync(0xffffffffu, valid);
-        if constexpr (DIRECT) {
-          const int kb = J % NB;
-          bool ok = true;
-          if (lane == 0 && J >= NB)
-            ok = wait(&sh.k_free[kb], ((J / NB) - 1) & 1, sh.abort) && wait(&sh.v_free[kb], ((J / NB) - 1) & 1, sh.abort);
-          run = __all_sync(0xffffffffu, ok);
-          if (!run) break;
-          if (lane < kPPB) sh.page_ok[kb * kPPB + lane] = valid;
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&sh.tile_full[kb], __popc(vm) * Y::REC);
-          __syncwarp();
-          if (valid) {
+        bool ok = true;
+        if (lane == 0 && round > 0) {
+          if constexpr (DIRECT)
+            ok = wait(&sh.k_free[buf], (round - 1) & 1, sh.abort) && wait(&sh.v_free[buf], (round - 1) & 1, sh.abort);
+          else
+            ok = wait(&sh.raw_empty[buf], (round - 1) & 1, sh.abort);
+        }
+        run = __all_sync(0xffffffffu, ok);
+        if (!run) break;
+        uint64_t* full = DIRECT ? &sh.tile_full[buf] : &sh.raw_full[buf];
+        if (lane == 0) {
+          sh.pages[buf] = static_cast<int>(vm);
+          mbar_arrive_expect_tx(full, __popc(vm) * Y::REC);
+        }
+        __syncwarp();
+        if (valid) {
+          if constexpr (DIRECT) {
             // 16 K rows and 16 V rows of 256 bytes, as two 128-byte halves each
             const int y = (blk * p.H + sg.kvh) * (2 * kBS), r0 = lane * kBS * 128;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              tma_load_2d(smem + Y::K_OFF + kb * kTile + hh * 16384 + r0, &rows, &sh.tile_full[kb], 128 * hh, y);
-              tma_load_2d(smem + Y::V_OFF + kb * kTile + hh * 16384 + r0, &rows, &sh.tile_full[kb], 128 * hh, y + kBS);
+              tma_load_2d(smem + Y::K_OFF + buf * kTile + hh * (kTile / 2) + r0, &rows, full, 128 * hh, y);
+              tma_load_2d(smem + Y::V_OFF + buf * kTile + hh * (kTile / 2) + r0, &rows, full, 128 * hh, y + kBS);
             }
-          }
-        } else {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h, ++gc) {
-            const int grp = gc % Y::RH, round = gc / Y::RH;
-            bool ok = true;
-            if (lane == 0 && round > 0) ok = wait(&sh.raw_empty[grp], (round - 1) & 1, sh.abort);
-            run = __all_sync(0xffffffffu, ok);
-            if (!run) break;
-            const int pp = lane - h * Y::HP;
-            const bool here = pp >= 0 && pp < Y::HP;
-            if (here) sh.page_ok[grp * Y::HP + pp] = valid;
-            __syncwarp();
-            if (lane == 0)
-              mbar_arrive_expect_tx(&sh.raw_full[grp], __popc((vm >> (h * Y::HP)) & ((1u << Y::HP) - 1u)) * Y::REC);
-            __syncwarp();
-            if (here && valid)
-              bulk_load(smem + Y::RAW_OFF + (grp * Y::HP + pp) * Y::REC,
-                        p.pages + (static_cast<long>(blk) * p.H + sg.kvh) * Y::REC, Y::REC, &sh.raw_full[grp]);
+          } else {
+            bulk_load(smem + Y::RAW_OFF + (buf * kPPB + lane) * Y::REC,
+                      p.pages + (static_cast<long>(blk) * p.H + sg.kvh) * Y::REC, Y::REC, full);
           }
         }
+        if (++buf == RING) { buf = 0; ++round; }
       }
     }
     if (!run && lane == 0) fail(p, sh.abort);
     // every copy issued must land before the CTA may exit
     if (lane == 0) {
-      if constexpr (DIRECT) {
-        for (int i = max(0, J - NB); i < J; ++i)
-          if (!mbar_drain(&sh.tile_full[i % NB], (i / NB) & 1)) record_fault(p.fault, KVQ_FAULT_TIMEOUT);
-      } else {
-        constexpr int RH = Y::RH > 0 ? Y::RH : 1;
-        for (int i = max(0, gc - RH); i < gc; ++i)
-          if (!mbar_drain(&sh.raw_full[i % RH], (i / RH) & 1)) record_fault(p.fault, KVQ_FAULT_TIMEOUT);
-      }
+      for (int i = max(0, J - RING); i < J; ++i)
+        if (!mbar_drain(DIRECT ? &sh.tile_full[i % RING] : &sh.raw_full[i % RING], (i / RING) & 1))
+          record_fault(p.fault, KVQ_FAULT_TIMEOUT);
     }
-  } else if (warp >= kConvWarp0) {
+  } else if (warp >= kConvWarp0 && warp < kOutWarp) {
     // ------------------------------------------------------------ converters
-    // thread (c, rr): 16-byte chunk c of rows rr and rr + 8 of every page; thread ct also looks
-    // after token ct of the block (its scale, its row's zeros)
+    // thread (c, rr): 16-byte chunk c of rows rr and rr + 8 of every page; K: thread ct < 64 also
+    // carries token ct's scales; 16-bit caches, V: token ct's zeros
     const bool isv = warp >= kConvWarp0 + 4;
     const int cw = (warp - kConvWarp0) & 3, ct = cw * 32 + lane;
     const int c = ct & 15, rr = ct >> 4;
     bool run = true;
-    int gc = 0;
+    const int nbuf = isv ? NBV : NBK;
+    int kb = 0, kround = 0, slot = 0, sround = 0, raw = 0, rround = 0;
     while (run && walk.next(p, sg)) {
       const int first = sg.n - sg.L;                          // first drafted position
-      for (int j = sg.j0; j < sg.j1; ++j, ++J) {
-        const int kb = J % NB, slot = J % kNQ;
+      for (int j = sg.j0; j < sg.j1; ++j) {
         bool ok = true;
-        if (isv) {
-          if (!DIRECT && J >= NB) ok = wait(&sh.v_free[kb], ((J / NB) - 1) & 1, sh.abort);
-        } else {
-          if (!DIRECT && J >= NB) ok = wait(&sh.k_free[kb], ((J / NB) - 1) & 1, sh.abort);
-          if (ok && J >= kNQ) ok = wait(&sh.kq_free[slot], ((J / kNQ) - 1) & 1, sh.abort);
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        const bool tail = j * kTreeBlk + kTreeBlk > first;    // holds drafted positions, or the end
-        int pok = 0;
-        bool nf = false;
-        float scale = 0.f;
         if constexpr (DIRECT) {
-          if (ok) ok = wait(&sh.tile_full[kb], (J / NB) & 1, sh.abort);
-          run = __all_sync(0xffffffffu, ok);
-          if (!run) break;
-#pragma unroll
-          for (int pp = 0; pp < kPPB; ++pp) pok |= (sh.page_ok[kb * kPPB + pp] ? 1 : 0) << pp;
-          if (isv && (tail || pok != (1 << kPPB) - 1)) {
+          if (!isv && sround > 0) ok = wait(&sh.kq_free[slot], (sround - 1) & 1, sh.abort);
+          if (ok) ok = wait(&sh.tile_full[kb], kround & 1, sh.abort);
+        } else {
+          ok = wait(&sh.raw_full[raw], rround & 1, sh.abort);
+          if (ok && kround > 0) ok = wait(isv ? &sh.v_free[kb] : &sh.k_free[kb], (kround - 1) & 1, sh.abort);
+          if (ok && !isv && sround > 0) ok = wait(&sh.kq_free[slot], (sround - 1) & 1, sh.abort);
+        }
+        run = __all_sync(0xffffffffu, ok);
+        if (!run) break;
+        const int pok = sh.pages[DIRECT ? kb : raw];
+        const bool tail = j * kTreeBlk + kTreeBlk > first;    // holds drafted positions, or the end
+        const bool whole = !tail && pok == kAll;
+        bool nf = false;
+        if constexpr (DIRECT) {
+          if (isv && !whole && ct < kTreeBlk) {
             const int pos = j * kTreeBlk + ct;
             const bool keep = pos < sg.n && ((pok >> (ct / kBS)) & 1);
             uint8_t* tile = smem + Y::V_OFF + kb * kTile;
             if (!keep || pos >= first) {
 #pragma unroll 4
               for (int cc = 0; cc < 16; ++cc) {
-                uint4* a = reinterpret_cast<uint4*>(tile + tile_off(ct, cc));
+                uint4* a = reinterpret_cast<uint4*>(tile + tile_off<kTreeBlk>(ct, cc));
                 uint4 u = keep ? *a : make_uint4(0, 0, 0, 0);
                 const bool drop = drop_nonfinite<BF>(u);
                 if (!keep || drop) *a = u;
@@ -463,149 +547,156 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
             }
           }
         } else {
-          uint8_t* tile = smem + (isv ? Y::V_OFF : Y::K_OFF) + kb * kTile + tile_off(rr, c) - rr * 128;
-#pragma unroll 1
-          for (int h = 0; h < 2 && ok; ++h) {
-            const int grp = (gc + h) % (Y::RH > 0 ? Y::RH : 1), round = (gc + h) / (Y::RH > 0 ? Y::RH : 1);
-            ok = wait(&sh.raw_full[grp], round & 1, sh.abort);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            const uint8_t* raw = smem + Y::RAW_OFF + grp * Y::HP * Y::REC;
-            uint2 w[Y::HP][2];
-            int hp = 0;
+          uint8_t* tile = smem + (isv ? Y::V_OFF : Y::K_OFF) + kb * kTile + tile_off<kTreeBlk>(rr, c) - rr * 128;
+          const uint8_t* src = smem + Y::RAW_OFF + raw * (kPPB * Y::REC);
+          const uint8_t* row = src + (isv ? Y::OFF_V : 0) + rr * Y::ROWB + 8 * c;
+          uint2 w[kPPB][2];
 #pragma unroll
-            for (int pp = 0; pp < Y::HP; ++pp) {
-              hp |= (sh.page_ok[grp * Y::HP + pp] ? 1 : 0) << pp;
+          for (int pp = 0; pp < kPPB; ++pp)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) w[pp][k] = *reinterpret_cast<const uint2*>(row + pp * Y::REC + 8 * k * Y::ROWB);
+          float kscale = 0.f, vscale = 0.f;
+          if constexpr (PT) {
+            if (!isv && ct < kTreeBlk) {
+              const float* sc = reinterpret_cast<const float*>(src + (ct >> 4) * Y::REC + Y::OFF_S) + (ct & 15);
+              kscale = sc[0];
+              vscale = sc[kBS];
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.raw_empty[raw]);
+          auto code16 = [&](const uint2& x) { return CD == KVQ_DTYPE_INT8 ? i8x8_to_f16(x) : e4m3x8_to_f16(x); };
+          if (whole) {
+#pragma unroll
+            for (int pp = 0; pp < kPPB; ++pp)
 #pragma unroll
               for (int k = 0; k < 2; ++k)
-                w[pp][k] = *reinterpret_cast<const uint2*>(raw + pp * Y::REC + (isv ? Y::OFF_V : 0) + (rr + 8 * k) * Y::ROWB + 8 * c);
-            }
-            if constexpr (PT) {
-              if ((ct >> 6) == h) {
-                const int pp = (ct & 63) >> 4;
-                scale = reinterpret_cast<const float*>(raw + pp * Y::REC + Y::OFF_S)[(isv ? kBS : 0) + (ct & 15)];
-              }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.raw_empty[grp]);
-            pok |= hp << (h * Y::HP);
-            const bool whole = !tail && hp == (1 << Y::HP) - 1;
+                *reinterpret_cast<uint4*>(tile + (pp * kBS + rr + 8 * k) * 128) = code16(w[pp][k]);
+          } else {
 #pragma unroll
-            for (int pp = 0; pp < Y::HP; ++pp)
+            for (int pp = 0; pp < kPPB; ++pp)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const int t = (h * Y::HP + pp) * kBS + rr + 8 * k;
-                uint4 u = CD == KVQ_DTYPE_INT8 ? i8x8_to_f16(w[pp][k]) : e4m3x8_to_f16(w[pp][k]);
-                if (!whole) {
-                  const int pos = j * kTreeBlk + t;
-                  if (!(((hp >> pp) & 1) && pos < sg.n)) u = make_uint4(0, 0, 0, 0);
-                  else if (CD == KVQ_DTYPE_FP8_E4M3 && isv && pos >= first) nf = drop_nonfinite<false>(u) || nf;
-                }
+                const int t = pp * kBS + rr + 8 * k, pos = j * kTreeBlk + t;
+                uint4 u = code16(w[pp][k]);
+                if (!(((pok >> pp) & 1) && pos < sg.n)) u = make_uint4(0, 0, 0, 0);
+                else if (CD == KVQ_DTYPE_FP8_E4M3 && isv && pos >= first) nf = drop_nonfinite<false>(u) || nf;
                 *reinterpret_cast<uint4*>(tile + t * 128) = u;
               }
           }
-          gc += 2;
-          run = __all_sync(0xffffffffu, ok);
-          if (!run) break;
           if constexpr (PT) {
-            const int pos = j * kTreeBlk + ct;
-            const bool keep = pos < sg.n && ((pok >> (ct / kBS)) & 1);
-            if (!isv) {
-              sh.ks[slot * kTreeBlk + ct] = keep ? scale : 0.f;
-            } else {
-              if (!keep) scale = 0.f;
-              if (pos >= first && !(fabsf(scale) <= 3.4e38f)) {   // an unusable drafted row
-                scale = 0.f;
-                nf = true;
+            if (!isv && ct < kTreeBlk) {                       // whole warps
+              bool sf = false;
+              if (!whole) {
+                const int pos = j * kTreeBlk + ct;
+                if (!(pos < sg.n && ((pok >> (ct / kBS)) & 1))) kscale = vscale = 0.f;
+                if (pos >= first && !(fabsf(vscale) <= 3.4e38f)) {   // an unusable drafted row
+                  vscale = 0.f;
+                  sf = true;
+                }
               }
-              sh.vs[kb * kTreeBlk + ct] = scale;
-              // V scales are >= 0: their bit patterns order as the values do (a NaN, in the
-              // prefix, above all of them: it must not set the exponent)
-              const unsigned m = __reduce_max_sync(0xffffffffu, scale <= 3.4e38f ? __float_as_uint(scale) : 0u);
-              if (lane == 0) sh.vmax[kb * 4 + cw] = __uint_as_float(m);
+              sh.ks[slot * kTreeBlk + ct] = kscale;
+              sh.vs[slot * kTreeBlk + ct] = vscale;
+              // V scales are >= 0: their bit patterns order as the values do (a NaN of the
+              // prefix lies above all of them: it must not set the exponent)
+              const unsigned m = __reduce_max_sync(0xffffffffu, vscale <= 3.4e38f ? __float_as_uint(vscale) : 0u);
+              sf = __any_sync(0xffffffffu, sf);
+              if (lane == 0) {
+                sh.vmax[slot * 4 + cw] = __uint_as_float(m);
+                sh.snf[slot * 4 + cw] = sf;
+              }
             }
           }
         }
-        const bool any_nf = __any_sync(0xffffffffu, nf);
-        if (isv && lane == 0) sh.vnf[kb * 4 + cw] = any_nf;
+        if (isv && tail) {
+          nf = __any_sync(0xffffffffu, nf);
+          if (lane == 0) sh.vnf[kb * 4 + cw] = nf;
+        }
         if (!isv && ct == 0) sh.pok[slot] = pok;
         tc::fence_async_shared();
         __syncwarp();
         if (lane == 0) {
-          if (isv) {
-            mbar_arrive(&sh.v_full[kb]);
-          } else {
-            mbar_arrive(&sh.k_full[kb]);
-            mbar_arrive(&sh.kq_full[slot]);
-          }
+          mbar_arrive(isv ? &sh.v_full[kb] : &sh.k_full[kb]);
+          if (!isv) mbar_arrive(&sh.kq_full[slot]);
         }
+        if (++kb == nbuf) { kb = 0; ++kround; }
+        if (++slot == kNQ) { slot = 0; ++sround; }
+        if (++raw == Y::RSD) { raw = 0; ++rround; }
       }
     }
     if (!run && lane == 0) fail(p, sh.abort);
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    // per unit: S of its first two blocks, then for each block P V and S two blocks ahead.  The
-    // tensor cores work in order, so S of block j + 2 may overwrite the columns P V of block j
-    // reads, and its completion says that P V of block j is complete too.
+  } else if (warp == kScoreWarp) {
+    // ------------------------------------------------------------ S = Q K^T
+    // (the whole warp runs the loop, so that descriptors stay in uniform registers)
     const uint32_t tiles = smem_u32(smem);
     constexpr uint32_t idS = tc::idesc_f16(BF, false, kTreeRows, kTreeBlk);
-    constexpr uint32_t idPV = tc::idesc_f16(BF, true, kTreeRows, kD);
-    if (lane == 0) {
-      bool ok = true;
-      int unit = 0;
-      auto scores = [&](int jj) -> bool {
-        const int kb = jj % NB;
-        if (!wait(&sh.k_full[kb], (jj / NB) & 1, sh.abort)) return false;
-        if (DIRECT && !wait(&sh.tile_full[kb], (jj / NB) & 1, sh.abort)) return false;
+    const uint64_t dq = first_kmajor(tiles + Y::Q_OFF), dk = first_kmajor(tiles + Y::K_OFF);
+    bool ok = true;
+    int unit = 0, kb = 0, kround = 0;
+    while (ok && walk.next(p, sg)) {
+      ok = __all_sync(0xffffffffu, wait(sh.q_ready, unit & 1, sh.abort));
+      for (int j = sg.j0; j < sg.j1 && ok; ++j, ++J) {
+        // the score buffer: P V of block J - 4 has read it
+        bool fine = J < kNS || wait(&sh.s_free[J & 3], ((J >> 2) - 1) & 1, sh.abort);
+        if (fine) fine = wait(DIRECT ? &sh.tile_full[kb] : &sh.k_full[kb], kround & 1, sh.abort);
+        ok = __all_sync(0xffffffffu, fine);
+        if (!ok) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          tc::mma_ss(tbase + 128 * (jj & 1), tc::desc_kmajor(tiles + Y::Q_OFF, kk),
-                     tc::desc_kmajor(tiles + Y::K_OFF + kb * kTile, kk), idS, kk > 0);
-        tc::commit(&sh.k_free[kb]);
-        tc::commit(&sh.s_full[jj & 1]);
-        return true;
-      };
-      while (ok && walk.next(p, sg)) {
-        const int nj = sg.j1 - sg.j0;
-        ok = wait(sh.q_ready, unit & 1, sh.abort);
-        tc::fence_after_sync();
-        if (ok) ok = scores(J);
-        if (ok && nj > 1) ok = scores(J + 1);
-        for (int i = 0; i < nj && ok; ++i) {
-          const int jj = J + i, kb = jj % NB, st = jj & 1;
-          if (!wait(&sh.v_full[kb], (jj / NB) & 1, sh.abort) || !wait(&sh.p_full[st], (jj >> 1) & 1, sh.abort)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
-#pragma unroll
-          for (int pa = 0; pa < (HILO ? 2 : 1); ++pa)
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc::mma_ts(tbase + kTmO + 128 * st, tbase + 128 * st + 16 * kk + 8 * pa,
-                         tc::desc_mnmajor(tiles + Y::V_OFF + kb * kTile, kk), idPV, i > 1 || pa > 0 || kk > 0);
-          tc::commit(&sh.v_free[kb]);
-          if (i == nj - 1) tc::commit(sh.o_full);
-          if (i + 2 < nj) ok = scores(jj + 2);
-        }
-        J += nj;
-        ++unit;
+          mma_ss_one(tbase + kTreeBlk * (J & 3), dq + step_kmajor<kTreeRows>(kk), dk + kb * (kTile / 16) + step_kmajor<kTreeBlk>(kk),
+                     idS, kk > 0);
+        commit_one(&sh.k_free[kb]);
+        commit_one(&sh.s_full[J & 3]);
+        if (++kb == NBK) { kb = 0; ++kround; }
       }
-      if (!ok) fail(p, sh.abort);
-      // one more commit covers every MMA issued above: TMEM is freed only after it arrives
-      tc::commit(sh.fin);
-      if (!mbar_drain(sh.fin, 0)) record_fault(p.fault, KVQ_FAULT_TIMEOUT);
+      ++unit;
     }
+    if (!ok && lane == 0) fail(p, sh.abort);
+    // one more commit covers every MMA issued above: TMEM is freed only after it arrives
+    commit_one(&sh.fin[0]);
+    if (!mbar_drain(&sh.fin[0], 0) && lane == 0) record_fault(p.fault, KVQ_FAULT_TIMEOUT);
     __syncwarp();
-  } else {
+  } else if (warp == kOutWarp) {
+    // ------------------------------------------------------------ O += P V
+    constexpr uint32_t idPV = tc::idesc_f16(BF, true, kTreeRows, kD);
+    const uint64_t dv = first_mnmajor(smem_u32(smem) + Y::V_OFF);
+    bool ok = true;
+    int vb = 0, vround = 0;
+    while (ok && walk.next(p, sg)) {
+      for (int j = sg.j0; j < sg.j1 && ok; ++j, ++J) {
+        const int st = J & 1;
+        bool fine = wait(&sh.v_full[vb], vround & 1, sh.abort);
+        if (fine) fine = wait(&sh.p_full[J & 3], (J >> 2) & 1, sh.abort);
+        ok = __all_sync(0xffffffffu, fine);
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int pa = 0; pa < (HILO ? 2 : 1); ++pa)
+#pragma unroll
+          for (int kk = 0; kk < kTreeBlk / 16; ++kk)
+            mma_ts_one(tbase + kTmO + 128 * st, tbase + kTreeBlk * (J & 3) + 16 * kk + 8 * pa, dv + vb * (kTile / 16) + kk * 128,
+                       idPV, j > sg.j0 + 1 || pa > 0 || kk > 0);
+        commit_one(&sh.v_free[vb]);
+        commit_one(&sh.s_free[J & 3]);
+        commit_one(&sh.pv_done[st]);
+        if (j == sg.j1 - 1) commit_one(sh.o_full);
+        if (++vb == NBV) { vb = 0; ++vround; }
+      }
+    }
+    if (!ok && lane == 0) fail(p, sh.abort);
+    commit_one(&sh.fin[1]);
+    if (!mbar_drain(&sh.fin[1], 0) && lane == 0) record_fault(p.fault, KVQ_FAULT_TIMEOUT);
+    __syncwarp();
+  } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------ softmax
     const int st = warp >> 2, quarter = warp & 3;
     const int r = 32 * quarter + lane;                        // row of the tile (TMEM lane)
     const uint32_t lanes = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t sbase = lanes + 128 * st, obase = lanes + kTmO + 128 * st;
+    const uint32_t obase = lanes + kTmO + 128 * st;
     float* ex = reinterpret_cast<float*>(smem + Y::Q_OFF);    // [2][2][128] at a unit's end
     int* exf = reinterpret_cast<int*>(ex + 512);              // [2] nonfinite drafted rows seen
-    int unit = 0, syncs = 0;
+    int unit = 0, syncs = 0, seen = 0;                        // seen: blocks of this stream
     bool ok = true;
     auto sync8 = [&]() -> bool {                              // the eight softmax warps
       __syncwarp();
@@ -676,7 +767,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(smem + Y::Q_OFF + tile_off(warp * 16 + 2 * i + (lane >> 4), c)) = u[i];
+          *reinterpret_cast<uint4*>(smem + Y::Q_OFF + tile_off<kTreeRows>(warp * 16 + 2 * i + (lane >> 4), c)) = u[i];
         tc::fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(sh.q_ready);
@@ -686,172 +777,147 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       const int tok = row_ok ? x / p.g : 0;
       const uint32_t* mrow = p.mask + (static_cast<long>(sg.q0) + tok) * p.mask_words;
       const int first = sg.n - sg.L;
-      // running maximum m (re-based when a score exceeds it by 2^8) and the exponent ev of the
-      // largest V scale so far: P holds e = 2^(x - m - ev) times the token's V scale, below 2^10;
-      // l and O accumulate in that domain
-      float m = -INFINITY, l = 0.f;
-      int ev = INT_MIN, nfseen = 0;
+      // Running maximum m, an integer, raised to the next one above a score that exceeds it by
+      // 2^8, so that every factor between two maxima is a power of two and re-basing is exact;
+      // ev the exponent of the largest V scale so far.  P holds e = 2^(x - off), off = m + ev, times
+      // the token's V scale, below 2^10; l and O accumulate in that domain.
+      float m = -INFINITY, moff = 0.f, l = 0.f;               // moff: m, or 0 before the first score
+      int ev = 0, nfseen = 0;                                 // (PT)
       bool begun = false;
       for (int j = sg.j0; j < sg.j1; ++j) {
         const int jj = J + j - sg.j0;
         if ((jj & 1) != st) continue;
-        const int kb = jj % NB, slot = jj % kNQ;
-        ok = wait(&sh.s_full[st], (jj >> 1) & 1, sh.abort) && wait(&sh.kq_full[slot], (jj / kNQ) & 1, sh.abort);
+        const int sb = jj & 3, slot = jj % kNQ;
+        const uint32_t sbase = lanes + kTreeBlk * sb;
+        ok = wait(&sh.kq_full[slot], (jj / kNQ) & 1, sh.abort) && wait(&sh.s_full[sb], (jj >> 2) & 1, sh.abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc::fence_after_sync();
         const int pok = sh.pok[slot];
-        const bool fast = j * kTreeBlk + kTreeBlk <= first && pok == (1 << kPPB) - 1;   // uniform
+        const bool fast = j * kTreeBlk + kTreeBlk <= first && pok == kAll;   // uniform
+        if (!fast && j * kTreeBlk + kTreeBlk > first) {
+          // drafted rows that hold infinities or NaN (the V converters' flags come with the tile)
+          const int kb = jj % NBV;
+          ok = __all_sync(0xffffffffu, wait(&sh.v_full[kb], (jj / NBV) & 1, sh.abort));
+          nfseen |= sh.vnf[kb * 4] | sh.vnf[kb * 4 + 1] | sh.vnf[kb * 4 + 2] | sh.vnf[kb * 4 + 3];
+          if (PT) nfseen |= sh.snf[slot * 4] | sh.snf[slot * 4 + 1];
+        }
+        // this stream's block before: its P V must be complete before O is touched (rare)
+        auto settle = [&]() {
+          if (seen > 0 && !wait(&sh.pv_done[st], (seen - 1) & 1, sh.abort)) ok = false;
+          tc::fence_after_sync();
+        };
         if (warp_ok) {
           const float* ks = sh.ks + slot * kTreeBlk;
-          const float* vsp = sh.vs + kb * kTreeBlk;
-          uint32_t ra[16], rb[16];
-          float m0 = -INFINITY, m1 = -INFINITY;
-          // --- pass 1: the largest score (times its K scale) of the row, 16 columns at a time
-          auto max16 = [&](const uint32_t* s16, int c0) {
-            if constexpr (PT) {
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(ks + c0 + i);
-                const float2 a = __fmul2_rn(make_float2(__uint_as_float(s16[i]), __uint_as_float(s16[i + 1])), make_float2(f.x, f.y));
-                const float2 b = __fmul2_rn(make_float2(__uint_as_float(s16[i + 2]), __uint_as_float(s16[i + 3])), make_float2(f.z, f.w));
-                m0 = max3(m0, a.x, a.y);
-                m1 = max3(m1, b.x, b.y);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                m0 = max3(m0, __uint_as_float(s16[i]), __uint_as_float(s16[i + 1]));
-                m1 = max3(m1, __uint_as_float(s16[i + 2]), __uint_as_float(s16[i + 3]));
-              }
-            }
-          };
-          if (fast) {
-            tc::ld16_issue(sbase, ra);
-#pragma unroll
-            for (int cc = 0; cc < 8; cc += 2) {
-              tc::ld_wait16(ra);
-              tc::ld16_issue(sbase + 16 * cc + 16, rb);
-              max16(ra, 16 * cc);
-              tc::ld_wait16(rb);
-              if (cc < 6) tc::ld16_issue(sbase + 16 * cc + 32, ra);
-              max16(rb, 16 * cc + 16);
-            }
-          } else {
-#pragma unroll 1
-            for (int cc = 0; cc < 8; ++cc) {
-              const uint32_t vis = column_bits(mrow, pok, j, cc >> 1, sg.n, sg.L) >> (16 * (cc & 1));
-              tc::ld16(sbase + 16 * cc, ra);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float a = __uint_as_float(ra[i]);
-                if constexpr (PT) a *= ks[16 * cc + i];
-                if ((vis >> i) & 1u) m0 = fmaxf(m0, a);
-              }
-            }
-          }
-          tc::ld16_issue(sbase, ra);                          // pass 2's first columns
-          const float mx = fmaxf(m0, m1) * qsc;
-          float fo = 1.f;
+          const float* vsp = sh.vs + slot * kTreeBlk;
           if constexpr (PT) {
-            ok = wait(&sh.v_full[kb], (jj / NB) & 1, sh.abort);
-            const float vmx = fmaxf(fmaxf(sh.vmax[kb * 4], sh.vmax[kb * 4 + 1]), fmaxf(sh.vmax[kb * 4 + 2], sh.vmax[kb * 4 + 3]));
-            if (vmx > 0.f) {
-              const int e = max(exponent_of(vmx), -100);
-              if (e > ev) {
-                if (ev != INT_MIN) fo = pow2i(ev - e);
-                ev = e;
-              }
-            }
-          } else if (!fast) {
-            ok = wait(&sh.v_full[kb], (jj / NB) & 1, sh.abort);
-          }
-          ok = __all_sync(0xffffffffu, ok);
-          if (!fast) nfseen |= sh.vnf[kb * 4] | sh.vnf[kb * 4 + 1] | sh.vnf[kb * 4 + 2] | sh.vnf[kb * 4 + 3];
-          if (mx > m + kRebase) {
-            fo *= m == -INFINITY ? 0.f : ex2(m - mx);
-            m = mx;
-          }
-          l *= fo;
-          if (begun && __any_sync(0xffffffffu, fo != 1.f)) {
-            // P V of this stream's block before is complete (its S was issued behind it)
-#pragma unroll 1
-            for (int cc = 0; cc < 8; ++cc) {
-              tc::ld16(obase + 16 * cc, rb);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) rb[i] = __float_as_uint(__uint_as_float(rb[i]) * fo);
-              st16(obase + 16 * cc, rb);
+            const float2 v2 = *reinterpret_cast<const float2*>(sh.vmax + slot * 4);
+            const float vmx = fmaxf(v2.x, v2.y);
+            const int e = max(exponent_of(vmx), -100);
+            if (!begun) {
+              ev = e;
+            } else if (e > ev) {
+              // (uniform) a larger V scale than before: l and O into the new domain
+              const float f = pow2i(ev - e);
+              ev = e;
+              l *= f;
+              settle();
+              scale_f32(obase, 8, f);
             }
           }
-          const float off = (m == -INFINITY ? 0.f : m) + (ev == INT_MIN ? 0.f : static_cast<float>(ev));
-          // --- pass 2: e = 2^(x - off), its sum, and P over the scores it came from
-          const float2 noff = make_float2(-off, -off), q2 = make_float2(qsc, qsc);
+          const float2 q2 = make_float2(qsc, qsc);
           float2 lsum = make_float2(0.f, 0.f);
-          auto p16 = [&](const uint32_t* s16, int c0, auto masked, uint32_t vis) {
-            uint32_t ph[8], pl[8];
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              float2 a = make_float2(__uint_as_float(s16[2 * i]), __uint_as_float(s16[2 * i + 1]));
-              float2 b = make_float2(__uint_as_float(s16[2 * i + 2]), __uint_as_float(s16[2 * i + 3]));
-              if constexpr (PT) {
-                const float4 f = *reinterpret_cast<const float4*>(ks + c0 + 2 * i);
-                a = __fmul2_rn(a, make_float2(f.x, f.y));
-                b = __fmul2_rn(b, make_float2(f.z, f.w));
-              }
-              a = __ffma2_rn(a, q2, noff);
-              b = __ffma2_rn(b, q2, noff);
-              if constexpr (decltype(masked)::value) {
-                if (!((vis >> (2 * i)) & 1u)) a.x = -INFINITY;
-                if (!((vis >> (2 * i + 1)) & 1u)) a.y = -INFINITY;
-                if (!((vis >> (2 * i + 2)) & 1u)) b.x = -INFINITY;
-                if (!((vis >> (2 * i + 3)) & 1u)) b.y = -INFINITY;
-              }
-              a = make_float2(ex2(a.x), ex2(a.y));
-              b = make_float2(ex2(b.x), ex2(b.y));
-              lsum = __fadd2_rn(lsum, __fadd2_rn(a, b));
-              if constexpr (PT) {
-                const float4 f = *reinterpret_cast<const float4*>(vsp + c0 + 2 * i);
-                a = __fmul2_rn(a, make_float2(f.x, f.y));
-                b = __fmul2_rn(b, make_float2(f.z, f.w));
-              }
-              if constexpr (HILO) {
-                split2<BF>(a, ph[i], pl[i]);
-                split2<BF>(b, ph[i + 1], pl[i + 1]);
-              } else {
-                ph[i] = pack2<BF>(a);
-                ph[i + 1] = pack2<BF>(b);
-              }
-            }
-            st8(sbase + c0, ph);
-            if constexpr (HILO) st8(sbase + c0 + 8, pl);
-          };
-          if (fast) {
-#pragma unroll
-            for (int cc = 0; cc < 8; cc += 2) {
-              tc::ld_wait16(ra);
-              tc::ld16_issue(sbase + 16 * cc + 16, rb);
-              p16(ra, 16 * cc, std::false_type{}, 0u);
-              tc::ld_wait16(rb);
-              if (cc < 6) tc::ld16_issue(sbase + 16 * cc + 32, ra);
-              p16(rb, 16 * cc + 16, std::false_type{}, 0u);
-            }
-          } else {
-            tc::ld_wait16(ra);
+          // --- one pass, 32 columns at a time: scores times the K scale, their maximum, e, its sum,
+          // and P over the scores it came from
+          auto block = [&](auto masked) {
 #pragma unroll 1
-            for (int cc = 0; cc < 8; ++cc) {
-              const uint32_t vis = column_bits(mrow, pok, j, cc >> 1, sg.n, sg.L) >> (16 * (cc & 1));
-              if (cc > 0) tc::ld16(sbase + 16 * cc, ra);
-              p16(ra, 16 * cc, std::true_type{}, vis);
+            for (int cc = 0; cc < kTreeBlk / 32; ++cc) {
+              uint32_t s[32];
+              tc::ld32(sbase + 32 * cc, s);
+              float2 t[16];
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                t[i] = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+                t[i + 1] = make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3]));
+                if constexpr (PT) {
+                  const float4 f = *reinterpret_cast<const float4*>(ks + 32 * cc + 2 * i);
+                  t[i] = __fmul2_rn(t[i], make_float2(f.x, f.y));
+                  t[i + 1] = __fmul2_rn(t[i + 1], make_float2(f.z, f.w));
+                }
+              }
+              if constexpr (decltype(masked)::value) {
+                const uint32_t vis = column_bits(mrow, pok, j, cc, sg.n, sg.L);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  if (!((vis >> (2 * i)) & 1u)) t[i].x = -INFINITY;
+                  if (!((vis >> (2 * i + 1)) & 1u)) t[i].y = -INFINITY;
+                }
+              }
+              float m0 = fmaxf(t[0].x, t[0].y), m1 = fmaxf(t[1].x, t[1].y);
+#pragma unroll
+              for (int i = 2; i < 16; i += 2) {
+                m0 = max3(m0, t[i].x, t[i].y);
+                m1 = max3(m1, t[i + 1].x, t[i + 1].y);
+              }
+              const float mx = fmaxf(m0, m1) * qsc;
+              if (__any_sync(0xffffffffu, mx > m + kRebase)) {
+                float f = 1.f;
+                if (mx > m + kRebase) {
+                  const float mn = ceilf(mx);
+                  f = m == -INFINITY ? 0.f : pow2i(static_cast<int>(fmaxf(m - mn, -1000.f)));
+                  m = moff = mn;
+                }
+                l *= f;
+                lsum = __fmul2_rn(lsum, make_float2(f, f));
+                tc::st_wait();
+                if (begun) {
+                  settle();
+                  scale_f32(obase, 8, f);
+                }
+                scale_p<BF, HILO>(sbase, 2 * cc, f);
+              }
+              const float off = PT ? moff + static_cast<float>(ev) : moff;
+              const float2 noff = make_float2(-off, -off);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t ph[8], pl[8];
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                  float2 a = __ffma2_rn(t[8 * h + i], q2, noff), b = __ffma2_rn(t[8 * h + i + 1], q2, noff);
+                  a = make_float2(ex2(a.x), ex2(a.y));
+                  b = make_float2(ex2(b.x), ex2(b.y));
+                  lsum = __fadd2_rn(lsum, __fadd2_rn(a, b));
+                  if constexpr (PT) {
+                    const float4 f = *reinterpret_cast<const float4*>(vsp + 32 * cc + 16 * h + 2 * i);
+                    a = __fmul2_rn(a, make_float2(f.x, f.y));
+                    b = __fmul2_rn(b, make_float2(f.z, f.w));
+                  }
+                  if constexpr (HILO) {
+                    split2<BF>(a, ph[i], pl[i]);
+                    split2<BF>(b, ph[i + 1], pl[i + 1]);
+                  } else {
+                    ph[i] = pack2<BF>(a);
+                    ph[i + 1] = pack2<BF>(b);
+                  }
+                }
+                st8(sbase + 32 * cc + 16 * h, ph);
+                if constexpr (HILO) st8(sbase + 32 * cc + 16 * h + 8, pl);
+                else (void)pl;
+              }
             }
-          }
+          };
+          if (fast) block(std::false_type{});
+          else block(std::true_type{});
           l += lsum.x + lsum.y;
           tc::st_wait();
         }
         begun = true;
+        ++seen;
+        ok = __all_sync(0xffffffffu, ok);
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sh.p_full[st]);
+          mbar_arrive(&sh.p_full[sb]);
           mbar_arrive(&sh.kq_free[slot]);
         }
         if (!ok) break;
@@ -865,7 +931,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       ++unit;
       if (!ok) break;
       tc::fence_after_sync();
-      ex[(2 * st) * 128 + r] = (m == -INFINITY ? 0.f : m) + (ev == INT_MIN ? 0.f : static_cast<float>(ev));
+      ex[(2 * st) * 128 + r] = moff + static_cast<float>(ev);
       ex[(2 * st + 1) * 128 + r] = l;
       if (threadIdx.x < 2) exf[threadIdx.x] = 0;
       ok = sync8();
@@ -958,7 +1024,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
   // ---------------------------------------------------------------- teardown
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kOutWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tbase, kTmemCols);
   }
@@ -994,27 +1060,58 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p) {
   // that starts before U1
   const int c0 = static_cast<int>(((U0 + 1) * p.ctas + W - 1) / W) - 1, c1 = static_cast<int>((U1 * p.ctas + W - 1) / W) - 1;
   if (c0 == c1) return;
-  float M = -INFINITY;
-  for (int c = c0; c <= c1; ++c) {
-    if (tree_range(W, c, p.ctas) == tree_range(W, c + 1, p.ctas)) continue;     // an empty range
-    const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * ((2L * c + (c == c0 ? 1 : 0)) * kTreeRows + r));
-    if (v.y != 0.f) M = fmaxf(M, v.x);
-  }
-  float L = 0.f;
+  // lane k describes CTA c0 + k; the partial rows are then read eight at a time, so that their
+  // loads overlap
+  float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; ++c) {
-    if (tree_range(W, c, p.ctas) == tree_range(W, c + 1, p.ctas)) continue;
-    const long row = (2L * c + (c == c0 ? 1 : 0)) * kTreeRows + r;
-    const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * row);
-    if (v.y == 0.f) continue;
-    const float w = ex2(v.x - M);
-    const float4 o = *reinterpret_cast<const float4*>(p.ws_o + row * kD + 4 * lane);
-    L = fmaf(v.y, w, L);
-    acc.x = fmaf(o.x, w, acc.x);
-    acc.y = fmaf(o.y, w, acc.y);
-    acc.z = fmaf(o.z, w, acc.z);
-    acc.w = fmaf(o.w, w, acc.w);
+  const float* o = p.ws_o + 4 * lane;
+  for (int k0 = c0; k0 <= c1; k0 += 32) {
+    const int c = k0 + lane;
+    long row = -1;
+    float mk = -INFINITY, lk = 0.f;
+    if (c <= c1 && tree_range(W, c, p.ctas) < tree_range(W, c + 1, p.ctas)) {
+      row = (2L * c + (c == c0 ? 1 : 0)) * kTreeRows + r;
+      const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * row);
+      lk = v.y;
+      if (lk != 0.f) mk = v.x;
+      else row = -1;                                          // nothing seen
+    }
+    float mx = mk;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    if (mx > M) {
+      const float f = M == -INFINITY ? 0.f : ex2(M - mx);
+      M = mx;
+      L *= f;
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    }
+    const float w = row >= 0 ? ex2(mk - M) : 0.f;
+    L = row >= 0 ? fmaf(lk, w, L) : L;
+    unsigned todo = __ballot_sync(0xffffffffu, row >= 0);
+    while (todo) {
+      float4 v[8];
+      float wt[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const int k = todo ? __ffs(todo) - 1 : -1;
+        todo &= todo - 1;
+        wt[t] = __shfl_sync(0xffffffffu, w, k & 31);
+        const long at = __shfl_sync(0xffffffffu, row, k & 31);
+        v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k >= 0) v[t] = *reinterpret_cast<const float4*>(o + at * kD);
+        else wt[t] = 0.f;
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        acc.x = fmaf(v[t].x, wt[t], acc.x);
+        acc.y = fmaf(v[t].y, wt[t], acc.y);
+        acc.z = fmaf(v[t].z, wt[t], acc.z);
+        acc.w = fmaf(v[t].w, wt[t], acc.w);
+      }
+    }
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
   const float inv = L != 0.f ? 1.f / L : 0.f;
   const long e0 = (static_cast<long>(s.q0) * p.Hq + i) * kD + 4 * lane;
   if (p.out_dtype == KVQ_DTYPE_FP32) {

@@ -276,29 +276,39 @@ def kvq_read_device_fault(desc, reset=True, stream=None):
     return int(out[0]), int(out[1])
 
 
-def _rows(t, heads, dim, what):
-    """Token stride of a [T][heads][dim] tensor whose rows are dense (a view into fused
-    projection rows is fine)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError("%s must be [tokens, %d, %d], got %s" % (what, heads, dim, tuple(t.shape)))
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+# The wrappers below run once per layer and step beside kernels of a few microseconds, so they
+# look at each tensor once and hand the addresses over as plain integers.
+def _raw_stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
+
+
+def _rows(t, what):
+    """(tokens, heads, dim, token stride) of a [T][heads][dim] tensor whose rows are dense (a view into
+    fused projection rows is fine)."""
+    try:
+        T, H, D = t.shape
+    except ValueError:
+        raise ValueError("%s must be [tokens, heads, dim], got %s" % (what, tuple(t.shape))) from None
+    a, b, c = t.stride()
+    if c != 1 or (H > 1 and b != D):
         raise ValueError("%s: the heads of a token must be contiguous" % what)
-    # (the stride of a single token, or of a one-token view, says nothing)
-    return max(t.stride(0), heads * dim) if t.shape[0] > 1 else heads * dim
+    # (the stride of a single token says nothing)
+    return T, H, D, a if T > 1 else H * D
 
 
-def _like(t, ref, what):
-    """t has the type and device of ref."""
-    if t.dtype != ref.dtype or t.device != ref.device:
-        raise TypeError("%s must be %s on %s, got %s on %s" % (what, ref.dtype, ref.device, t.dtype, t.device))
-    return t
-
-
-def _count(t, n, what):
-    """Index tensor of n entries (contiguous int32)."""
+def _index(t, n, what):
+    """Address of an index tensor of n entries (contiguous int32)."""
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise TypeError("%s must be contiguous int32" % what)
     if t.numel() != n:
         raise ValueError("%s must have %d entries, got %d" % (what, n, t.numel()))
-    return _i32(t)
+    return t.data_ptr()
+
+
+_ACT_CODE = {torch.bfloat16: 0, torch.float16: 1}
+_OUT_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 def kvq_rope_frequencies(rope):
@@ -312,64 +322,86 @@ def kvq_rope_frequencies(rope):
 def kvq_rope(rope, freqs, positions, q=None, k=None, q_out=None, k_out=None, stream=None):
     """Rotate q [T, Hq, D] and / or k [T, H, D] (token strides as they are) into q_out / k_out
     (given, or allocated dense); an output may be its input."""
-    ref = q if q is not None else k
-    T, D = ref.shape[0], ref.shape[2]
+    act = q.dtype if q is not None else k.dtype
+    if act not in _ACT_CODE:
+        raise TypeError("activations must be bfloat16 or float16, got %s" % act)
+    T = D = None
     args = []
-    outs = []
     for x, out, what in ((q, q_out, "q"), (k, k_out, "k")):
         if x is None:
-            args += [None, 0, 0, None, 0]
-            outs.append(None)
+            args += (None, 0, 0, None, 0)
             continue
-        if x.shape[0] != T:
-            raise ValueError("q and k must have the same number of tokens")
-        xs = _rows(_like(x, ref, what), x.shape[1], D, what)
+        Tx, H, Dx, xs = _rows(x, what)
+        if T is None:
+            T, D = Tx, Dx
+        if Tx != T or Dx != D:
+            raise ValueError("q and k must have the same tokens and head_dim")
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        elif out.shape != x.shape:
-            raise ValueError("%s_out must have the shape of %s" % (what, what))
-        args += [_ptr(x), xs, int(x.shape[1]), _ptr(out), _rows(_like(out, x, what + "_out"), x.shape[1], D, what + "_out")]
-        outs.append(out)
-    _check(lib.kvq_rope(ctypes.byref(rope), _ptr(freqs), DTYPE[_act(ref)], D, _ptr(_count(positions, T, "positions")), T,
-                        *args, _stream(stream)), "kvq_rope")
-    return tuple(outs)
+            out = torch.empty_like(x)                  # dense
+            os = H * D
+        else:
+            shape = _rows(out, what + "_out")
+            if shape[:3] != (T, H, D):
+                raise ValueError("%s_out must have the shape of %s" % (what, what))
+            os = shape[3]
+        if x.dtype != act or out.dtype != act:
+            raise TypeError("q, k and their outputs must have one type")
+        args += (x.data_ptr(), xs, H, out.data_ptr(), os)
+        if x is q:
+            q_out = out
+        else:
+            k_out = out
+    st = lib.kvq_rope(ctypes.byref(rope), freqs.data_ptr(), _ACT_CODE[act], D, _index(positions, T, "positions"), T, *args,
+                      _raw_stream(stream))
+    if st:
+        _check(st, "kvq_rope")
+    return (q_out if q is not None else None), (k_out if k is not None else None)
 
 
 def kvq_rope_write(desc, rope, freqs, positions, q, k_new, v_new, slot_mapping, q_out=None, stream=None):
     """kvq_rope of q and k_new, then kvq_write of the rotated keys and of v_new, in one launch.
     Returns q_out (None without q)."""
-    T, H, D = k_new.shape[0], desc.num_kv_heads, desc.head_dim
-    if DTYPE[_act(k_new)] != desc.act_dtype:
-        raise TypeError("k_new must have the cache's activation type")
-    ks = _rows(k_new, H, D, "k_new")
-    vs = _rows(_like(v_new, k_new, "v_new"), H, D, "v_new")
-    if v_new.shape[0] != T or (q is not None and q.shape[0] != T):
-        raise ValueError("q, k_new and v_new must have the same number of tokens")
-    qa = [None, 0, 0, None, 0]
+    T, H, D, ks = _rows(k_new, "k_new")
+    Tv, Hv, Dv, vs = _rows(v_new, "v_new")
+    act = k_new.dtype
+    if _ACT_CODE.get(act) != desc.act_dtype or v_new.dtype != act:
+        raise TypeError("k_new and v_new must have the cache's activation type")
+    if Tv != T or H != desc.num_kv_heads or Hv != H or D != desc.head_dim or Dv != D:
+        raise ValueError("k_new and v_new must be [tokens, %d, %d]" % (desc.num_kv_heads, desc.head_dim))
+    qp, qs, hq, qop, qos = None, 0, 0, None, 0
     if q is not None:
-        hq = int(q.shape[1])
+        Tq, hq, Dq, qs = _rows(q, "q")
+        if Tq != T or Dq != D:
+            raise ValueError("q must have the tokens and head_dim of k_new")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have the shape of q")
-        qa = [_ptr(q), _rows(_like(q, k_new, "q"), hq, D, "q"), hq, _ptr(q_out),
-              _rows(_like(q_out, k_new, "q_out"), hq, D, "q_out")]
-    _check(lib.kvq_rope_write(ctypes.byref(desc), ctypes.byref(rope), _ptr(freqs),
-                              _ptr(_count(positions, T, "positions")), T, *qa, _ptr(k_new), ks, _ptr(v_new), vs,
-                              _ptr(_count(slot_mapping, T, "slot_mapping")), _stream(stream)), "kvq_rope_write")
+            q_out = torch.empty_like(q)                # dense
+            qos = hq * D
+        else:
+            To, ho, Do, qos = _rows(q_out, "q_out")
+            if (To, ho, Do) != (T, hq, D):
+                raise ValueError("q_out must have the shape of q")
+        if q.dtype != act or q_out.dtype != act:
+            raise TypeError("q and q_out must have the cache's activation type")
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    st = lib.kvq_rope_write(ctypes.byref(desc), ctypes.byref(rope), freqs.data_ptr(), _index(positions, T, "positions"), T,
+                            qp, qs, hq, qop, qos, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+                            _index(slot_mapping, T, "slot_mapping"), _raw_stream(stream))
+    if st:
+        _check(st, "kvq_rope_write")
     return q_out
 
 
 def kvq_gather(desc, slots, k_out, v_out, stream=None):
     """K and V rows of the listed cache slots, dequantized to the activation type."""
-    n = int(slots.numel())
+    n = slots.numel()
     for t, what in ((k_out, "k_out"), (v_out, "v_out")):
-        if tuple(t.shape) != (n, desc.num_kv_heads, desc.head_dim) or not t.is_contiguous():
+        if t.shape != (n, desc.num_kv_heads, desc.head_dim) or not t.is_contiguous():
             raise ValueError("%s must be contiguous [%d, %d, %d]" % (what, n, desc.num_kv_heads, desc.head_dim))
-        if DTYPE[_act(t)] != desc.act_dtype:
+        if _ACT_CODE.get(t.dtype) != desc.act_dtype:
             raise TypeError("%s must have the cache's activation type" % what)
-    _check(lib.kvq_gather(ctypes.byref(desc), _ptr(_i32(slots)), n, _ptr(k_out), _ptr(v_out), _stream(stream)),
-           "kvq_gather")
+    st = lib.kvq_gather(ctypes.byref(desc), _index(slots, n, "slots"), n, k_out.data_ptr(), v_out.data_ptr(), _raw_stream(stream))
+    if st:
+        _check(st, "kvq_gather")
     return k_out, v_out
 
 
@@ -385,37 +417,42 @@ def kvq_tree_attention(desc, q, q_start, max_tree, tree_mask, block_tables, cont
     """Attention of each sequence's drafted tokens (rows q_start[b] .. q_start[b+1]-1 of q, the newest
     cached positions) over the cached prefix and the drafted tokens its mask row names.  tree_mask:
     int32 [tokens, words], the bits of the C ABI's uint32."""
-    T, Hq, D = q.shape
-    if D != desc.head_dim or DTYPE[_act(q)] != desc.act_dtype or not q.is_contiguous():
+    T, Hq, D, _ = _rows(q, "q")
+    if D != desc.head_dim or _ACT_CODE.get(q.dtype) != desc.act_dtype or not q.is_contiguous():
         raise ValueError("q must be contiguous [tokens, heads, %d] of the cache's activation type" % desc.head_dim)
-    if out.shape != q.shape or not out.is_contiguous():
+    if out.shape != (T, Hq, D) or not out.is_contiguous():
         raise ValueError("out must be contiguous and have the shape of q")
-    if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
-        raise ValueError("tree_mask must be [tokens, words]")
-    B = int(q_start.numel()) - 1
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("block_tables must be [%d, blocks]" % B)
-    out_dt = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}[out.dtype]
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib.kvq_tree_attention(
-        ctypes.byref(desc), _ptr(q), T, B, Hq, _ptr(_i32(q_start)), int(max_tree), _ptr(_i32(tree_mask)),
-        int(tree_mask.shape[1]), _ptr(_i32(block_tables)), int(block_tables.shape[1]),
-        _ptr(_count(context_lens, B, "context_lens")), int(max_context), float(softmax_scale), _ptr(out), DTYPE[out_dt],
-        _ptr(workspace), ws_bytes, _stream(stream)), "kvq_tree_attention")
+    B = context_lens.numel()
+    if tree_mask.dim() != 2 or block_tables.dim() != 2:
+        raise ValueError("tree_mask must be [tokens, words] and block_tables [batch, blocks]")
+    words, blocks = tree_mask.shape[1], block_tables.shape[1]
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = lib.kvq_tree_attention(
+        ctypes.byref(desc), q.data_ptr(), T, B, Hq, _index(q_start, B + 1, "q_start"), max_tree,
+        _index(tree_mask, T * words, "tree_mask"), words, _index(block_tables, B * blocks, "block_tables"), blocks,
+        _index(context_lens, B, "context_lens"), max_context, softmax_scale, out.data_ptr(), _OUT_CODE[out.dtype], ws, ws_bytes,
+        _raw_stream(stream))
+    if st:
+        _check(st, "kvq_tree_attention")
     return out
 
 
 def kvq_tree_commit(desc, path, accepted, q_start, block_tables, context_lens, new_lens=None, stream=None):
     """Move the cache rows of each sequence's accepted path (drafted indexes path[b, :accepted[b]]) to the
     first drafted positions; new_lens receives the new context lengths."""
-    B = int(accepted.numel())
-    if path.dim() != 2 or path.shape[0] != B or block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("path and block_tables must have one row per sequence")
-    _check(lib.kvq_tree_commit(
-        ctypes.byref(desc), _ptr(_i32(path)), int(path.shape[1]), _ptr(_i32(accepted)), B,
-        _ptr(_count(q_start, B + 1, "q_start")), _ptr(_i32(block_tables)), int(block_tables.shape[1]),
-        _ptr(_count(context_lens, B, "context_lens")),
-        None if new_lens is None else _ptr(_count(new_lens, B, "new_lens")), _stream(stream)), "kvq_tree_commit")
+    B = accepted.numel()
+    if path.dim() != 2 or block_tables.dim() != 2:
+        raise ValueError("path must be [batch, accepted at most] and block_tables [batch, blocks]")
+    most, blocks = path.shape[1], block_tables.shape[1]
+    st = lib.kvq_tree_commit(
+        ctypes.byref(desc), _index(path, B * most, "path"), most, _index(accepted, B, "accepted"), B,
+        _index(q_start, B + 1, "q_start"), _index(block_tables, B * blocks, "block_tables"), blocks,
+        _index(context_lens, B, "context_lens"), None if new_lens is None else _index(new_lens, B, "new_lens"),
+        _raw_stream(stream))
+    if st:
+        _check(st, "kvq_tree_commit")
     return new_lens
 
 
@@ -536,12 +573,12 @@ class PagedKVCache:
 
     def gather(self, slots, k_out=None, v_out=None, stream=None):
         """(K, V) rows of the listed slots, [rows, H, D] of the activation type."""
-        shape = (int(slots.numel()), self.num_kv_heads, self.head_dim)
-        dt = torch.bfloat16 if self.act_dtype == "bf16" else torch.float16
         if k_out is None:
+            shape = (slots.numel(), self.num_kv_heads, self.head_dim)
+            dt = torch.bfloat16 if self.act_dtype == "bf16" else torch.float16
             k_out = torch.empty(shape, dtype=dt, device=self.device)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=dt, device=self.device)
+            v_out = torch.empty_like(k_out)
         return kvq_gather(self.desc, slots, k_out, v_out, stream)
 
     def tree_workspace_size(self, batch, num_q_heads, max_tree, max_context):
@@ -550,9 +587,9 @@ class PagedKVCache:
     def tree_attention(self, q, q_start, max_tree, tree_mask, block_tables, context_lens, max_context, out=None,
                        out_dtype=torch.float32, workspace=None, softmax_scale=0.0, stream=None):
         if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+            out = torch.empty_like(q, dtype=out_dtype)
         if workspace is None:
-            n = self.tree_workspace_size(int(q_start.numel()) - 1, q.shape[1], max_tree, max_context)
+            n = self.tree_workspace_size(context_lens.numel(), q.shape[1], max_tree, max_context)
             workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device) if n else None
         return kvq_tree_attention(self.desc, q, q_start, max_tree, tree_mask, block_tables, context_lens,
                                   max_context, out, workspace, softmax_scale, stream)
