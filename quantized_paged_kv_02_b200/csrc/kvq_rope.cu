@@ -10,12 +10,13 @@
 // binary32 once.
 //
 // What bounds it: bytes (16-bit rows in, 16-bit rows and codes out; 3 flops per element), so
-// the work per element is kept below the copy's.  One CTA takes one token, whose cosines and
-// sines (at most 64 pairs) are computed once by as many threads, into shared memory, while the
-// first rows are on their way; every head then shares them.  D / 16 lanes hold one row, lane
+// the work per element is kept below the copy's.  A CTA takes up to four tokens, whose cosines
+// and sines (at most 64 pairs each) are computed once, one per thread, into shared memory, while
+// the first rows are on their way; every head then shares them.  D / 16 lanes hold one row, lane
 // i the 16-byte chunks i and i + D/16 (in the half layout with a partly rotated head, i and
 // i + rot/16), so both elements of a pair are always in one lane, each load of a lane group is
-// contiguous, and the rotation may run in place.  The quantizers are kvq_write's, fed
+// contiguous, and the rotation may run in place.  The rows of a CTA's tokens form one list, 32 (64
+// for head_dim 64) at a time, the loads of the next two turns in flight.  The quantizers are kvq_write's, fed
 // with the rotated binary32 values (no rounding to 16 bits in between).
 #include <algorithm>
 #include <climits>
@@ -28,6 +29,7 @@ namespace kvq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;       // tokens per CTA at most
 constexpr int kNoCache = -1;         // CD of kvq_rope: K rows go to k_out
 
 struct RopeParams {
@@ -79,18 +81,21 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c, const float* x,
   *reinterpret_cast<uint2*>(row + 8 * c) = w;
 }
 
-// grid (T, slices): token blockIdx.x; slice y takes every gridDim.y-th group of
-// kRopeThreads / LPR rows.  Rows: Hq of q, H of k, and with a cache H of v.
+// grid (ceil(T / tokens), slices): tokens blockIdx.x * tokens ..; slice y takes every gridDim.y-th
+// group of kRopeThreads / LPR entries of their row list.  Rows of a token: Hq of q, H of k, and
+// with a cache H of v.
 template <typename TA, int CD, int D, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(RopeParams p, int T, int tokens) {
   constexpr int LPR = D / 16;                 // lanes per row, two 16-byte chunks each
-  constexpr int RPB = kRopeThreads / LPR;     // rows per pass of the CTA
+  constexpr int RPB = kRopeThreads / LPR;     // rows per turn of the CTA
   constexpr bool CACHE = CD != kNoCache;
   constexpr bool CODES = CD == KVQ_DTYPE_INT8 || CD == KVQ_DTYPE_FP8_E4M3;
-  __shared__ __align__(16) float cosv[D / 2];
-  __shared__ __align__(16) float sinv[D / 2];
-  const int t = blockIdx.x, l = threadIdx.x % LPR;
-  const int rows = p.Hq + (CACHE ? 2 : 1) * p.H;
+  constexpr int AHEAD = 2;                    // turns whose loads are in flight
+  __shared__ __align__(16) float cosv[kRopeTokens][D / 2];
+  __shared__ __align__(16) float sinv[kRopeTokens][D / 2];
+  __shared__ int blk_of[kRopeTokens], off_of[kRopeTokens];   // (a cache) block, or -1: nothing stored
+  const int t0 = blockIdx.x * tokens, nt = min(tokens, T - t0), l = threadIdx.x % LPR;
+  const int rows = p.Hq + (CACHE ? 2 : 1) * p.H, total = nt * rows;
   const int pairs = p.rot / 2;
 
   int c0, c1, p0, p1;                         // the lane's chunks, and their first pairs
@@ -111,21 +116,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
     p1 = 4 * c1;
   }
 
-  int slot = -1;
-  uint8_t* rec0 = nullptr;                    // record of (block, head 0); heads follow
-  int off = 0;
-  if constexpr (CACHE) {
-    slot = p.slots[t];
-    const long nslots = static_cast<long>(p.NB) * p.bs;
-    if (blockIdx.y == 0 && threadIdx.x == 0 && (slot < -1 || slot >= nslots)) record_fault(p.fault, KVQ_FAULT_SLOT);
-    if (slot < 0 || slot >= nslots) slot = -1;
-    if (slot >= 0) {
-      const int blk = slot / p.bs;
-      off = slot - blk * p.bs;
-      rec0 = p.pages + static_cast<long>(blk) * p.H * p.record;
-    }
-  }
-  auto source = [&](int r) -> const uint4* {
+  // entry `at` of the list: token t0 + tk, row r of it
+  const int step = gridDim.y * RPB, start = blockIdx.y * RPB;
+  auto advance = [&](int& tk, int& r) {
+    r += step;
+    while (r >= rows && tk < nt) { r -= rows; ++tk; }
+  };
+  auto source = [&](int tk, int r) -> const uint4* {
+    const long t = t0 + tk;
     const void* base;
     long at;
     if (r < p.Hq) { base = p.q; at = t * p.q_stride + static_cast<long>(r) * D; }
@@ -133,38 +131,51 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
     else { base = p.v; at = t * p.v_stride + static_cast<long>(r - p.Hq - p.H) * D; }
     return reinterpret_cast<const uint4*>(static_cast<const TA*>(base) + at);
   };
-  // rows whose result is stored: every q row, and K / V rows with somewhere to go
-  auto wanted = [&](int r) { return r < rows && (r < p.Hq || !CACHE || slot >= 0); };
-
-  int r = blockIdx.y * RPB + threadIdx.x / LPR;
-  const int step = gridDim.y * RPB;
-  uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-  if (wanted(r)) { u0 = source(r)[c0]; u1 = source(r)[c1]; }
-  for (int i = threadIdx.x; i < pairs; i += kRopeThreads) {
+  int tk = 0, r = start + threadIdx.x / LPR;
+  while (r >= rows && tk < nt) { r -= rows; ++tk; }
+  int ltk = tk, lr = r;                       // what is loaded next
+  uint4 u[AHEAD][2];
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a) {
+    u[a][0] = u[a][1] = make_uint4(0, 0, 0, 0);
+    if (ltk < nt) {
+      const uint4* src = source(ltk, lr);
+      u[a][0] = src[c0];
+      u[a][1] = src[c1];
+    }
+    advance(ltk, lr);
+  }
+  if constexpr (CACHE) {
+    if (threadIdx.x < nt) {
+      const int slot = p.slots[t0 + threadIdx.x];
+      const bool in = slot >= 0 && slot < static_cast<long>(p.NB) * p.bs;
+      if (!in && slot != -1 && blockIdx.y == 0) record_fault(p.fault, KVQ_FAULT_SLOT);
+      blk_of[threadIdx.x] = in ? slot / p.bs : -1;
+      off_of[threadIdx.x] = in ? slot % p.bs : 0;
+    }
+  }
+  for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
     constexpr double kInvTwoPi = 0.15915494309189533577;
-    const double turn = static_cast<double>(p.pos[t]) * p.freqs[i] * kInvTwoPi;
+    const int k = i / pairs, f = i - k * pairs;
+    const double turn = static_cast<double>(p.pos[t0 + k]) * p.freqs[f] * kInvTwoPi;
     double sn, cs;
     sincospi(2.0 * (turn - rint(turn)), &sn, &cs);
-    cosv[i] = static_cast<float>(cs * p.mscale);
-    sinv[i] = static_cast<float>(sn * p.mscale);
+    cosv[k][f] = static_cast<float>(cs * p.mscale);
+    sinv[k][f] = static_cast<float>(sn * p.mscale);
   }
   __syncthreads();
-  float cs[8], sn[8];
-  if (turns0) {
-    *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(cosv + p0);
-    *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(sinv + p0);
-  }
-  if (turns1) {
-    *reinterpret_cast<float4*>(cs + 4) = *reinterpret_cast<const float4*>(cosv + p1);
-    *reinterpret_cast<float4*>(sn + 4) = *reinterpret_cast<const float4*>(sinv + p1);
-  }
 
-  // the trip count is the same for every thread of the CTA (the shuffles below need whole
-  // warps): rows past the end stand in with zeros and store nothing
-  for (int base = blockIdx.y * RPB; base < rows; base += step, r += step) {
-    const uint4 w0 = u0, w1 = u1;
-    if (wanted(r + step)) { u0 = source(r + step)[c0]; u1 = source(r + step)[c1]; }
-    const bool want = wanted(r), is_q = r < p.Hq, is_v = r >= p.Hq + p.H;
+  // one entry; then the load of the entry two turns on into the registers it leaves
+  auto entry = [&](uint4 (&u)[2]) {
+    const uint4 w0 = u[0], w1 = u[1];
+    if (ltk < nt) {
+      const uint4* src = source(ltk, lr);
+      u[0] = src[c0];
+      u[1] = src[c1];
+    }
+    advance(ltk, lr);
+    const bool have = tk < nt, is_q = r < p.Hq, is_v = r >= p.Hq + p.H;
+    const int k = have ? tk : 0;
     float x[16];
     unpack8<TA>(w0, x);
     unpack8<TA>(w1, x + 8);
@@ -172,39 +183,51 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
       if constexpr (HALF) {
         if (turns0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float a = x[i], b = x[i + 8];
-            x[i] = fmaf(a, cs[i], -b * sn[i]);
-            x[i + 8] = fmaf(b, cs[i], a * sn[i]);
+          for (int i = 0; i < 8; i += 4) {
+            const float4 c4 = *reinterpret_cast<const float4*>(&cosv[k][p0 + i]), s4 = *reinterpret_cast<const float4*>(&sinv[k][p0 + i]);
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const float2 a = make_float2(x[i + e], x[i + e + 1]), b = make_float2(x[i + e + 8], x[i + e + 9]);
+              const float2 c = e ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+              const float2 s = e ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
+              const float2 y = __ffma2_rn(a, c, __fmul2_rn(b, make_float2(-s.x, -s.y))), z = __ffma2_rn(b, c, __fmul2_rn(a, s));
+              x[i + e] = y.x;
+              x[i + e + 1] = y.y;
+              x[i + e + 8] = z.x;
+              x[i + e + 9] = z.y;
+            }
           }
         }
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 0 ? turns0 : turns1) {
+            const int at = h == 0 ? p0 : p1;
+            const float4 c4 = *reinterpret_cast<const float4*>(&cosv[k][at]), s4 = *reinterpret_cast<const float4*>(&sinv[k][at]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float a = x[8 * h + 2 * i], b = x[8 * h + 2 * i + 1];
-              x[8 * h + 2 * i] = fmaf(a, cs[4 * h + i], -b * sn[4 * h + i]);
-              x[8 * h + 2 * i + 1] = fmaf(b, cs[4 * h + i], a * sn[4 * h + i]);
+              const float a = x[8 * h + 2 * i], b = x[8 * h + 2 * i + 1], c = (&c4.x)[i], s = (&s4.x)[i];
+              x[8 * h + 2 * i] = fmaf(a, c, -b * s);
+              x[8 * h + 2 * i + 1] = fmaf(b, c, a * s);
             }
           }
         }
       }
     }
-    if (is_q || !CACHE) {
-      if (want) {
-        uint4* dst = is_q ? reinterpret_cast<uint4*>(static_cast<TA*>(p.q_out) + t * p.qo_stride + static_cast<long>(r) * D)
-                          : reinterpret_cast<uint4*>(static_cast<TA*>(p.k_out) + t * p.ko_stride + static_cast<long>(r - p.Hq) * D);
-        dst[c0] = turns0 ? pack8<TA>(x) : w0;
-        dst[c1] = turns1 ? pack8<TA>(x + 8) : w1;
-      }
+    if ((is_q || !CACHE) && have) {
+      const long t = t0 + tk;
+      uint4* dst = is_q ? reinterpret_cast<uint4*>(static_cast<TA*>(p.q_out) + t * p.qo_stride + static_cast<long>(r) * D)
+                        : reinterpret_cast<uint4*>(static_cast<TA*>(p.k_out) + t * p.ko_stride + static_cast<long>(r - p.Hq) * D);
+      dst[c0] = turns0 ? pack8<TA>(x) : w0;
+      dst[c1] = turns1 ? pack8<TA>(x + 8) : w1;
     }
-    if constexpr (CACHE) {
+    if constexpr (CACHE) if (__any_sync(0xffffffffu, have && !is_q)) {   // (most warps hold q rows only)
+      const int blk = blk_of[k], off = off_of[k];
       const int h = r - p.Hq - (is_v ? p.H : 0);
-      uint8_t* rec = rec0 + static_cast<long>(h) * p.record;
+      const bool keep = have && !is_q && blk >= 0;
+      uint8_t* rec = p.pages + (static_cast<long>(blk) * p.H + h) * p.record;
       if constexpr (CODES) {
-        // one pass in 32 rows a warp may hold q rows too: they take part in the maximum only
+        // (a warp may hold q rows too: they take part in the maximum only)
         const bool per_token = p.mode == KVQ_SCALE_PER_TOKEN_HEAD;
         float s = 0.f;
         if (per_token) {
@@ -215,7 +238,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
           for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           s = div_rn(m, QMax<CD>::v);
         }
-        if (want && !is_q) {
+        if (keep) {
           const float* st = is_v ? p.v_static : p.k_static;
           const float* chan = nullptr;
           if (p.mode == KVQ_SCALE_PER_HEAD) s = st[h];
@@ -226,12 +249,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
           store_codes<CD, D>(row, c0, x, s, per_token, chan);
           store_codes<CD, D>(row, c1, x + 8, s, per_token, chan);
         }
-      } else if (want && !is_q) {
+      } else if (keep) {
         uint4* row = reinterpret_cast<uint4*>(rec + (is_v ? p.off_v : 0) + off * 2 * D);
         row[c0] = !is_v && turns0 ? pack8<TA>(x) : w0;
         row[c1] = !is_v && turns1 ? pack8<TA>(x + 8) : w1;
       }
     }
+    advance(tk, r);
+  };
+  // the trip count is the same for every thread of the CTA (the shuffles need whole warps): entries
+  // past the end of the list stand in with zeros and store nothing
+  for (int base = start; base < total; base += 2 * step) {
+    entry(u[0]);
+    if (base + step < total) entry(u[1]);
   }
 }
 
@@ -239,12 +269,15 @@ template <typename TA, int CD, int D>
 cudaError_t launch_layout(const RopeParams& p, bool half, int T, cudaStream_t s) {
   const int rpb = kRopeThreads / (D / 16);
   const int rows = p.Hq + (CD == kNoCache ? 1 : 2) * p.H;
-  const int passes = (rows + rpb - 1) / rpb;
-  // few tokens: the passes of a token go to CTAs of their own, until every SM has work
-  const int slices = std::max(1, std::min(passes, 2 * device_sm_count() / std::max(T, 1)));
-  const dim3 grid(T, slices);
-  if (half) rope_kernel<TA, CD, D, true><<<grid, kRopeThreads, 0, s>>>(p);
-  else rope_kernel<TA, CD, D, false><<<grid, kRopeThreads, 0, s>>>(p);
+  // one token per CTA until every SM has three CTAs, then up to four; with fewer tokens than that
+  // a token's rows go to CTAs of their own
+  const int sms = device_sm_count(), passes = (rows + rpb - 1) / rpb;
+  const int tokens = std::max(1, std::min(kRopeTokens, T / (3 * sms)));
+  const int ctas = (T + tokens - 1) / tokens;
+  const int slices = std::max(1, std::min(passes, 2 * sms / std::max(ctas, 1)));
+  const dim3 grid(ctas, slices);
+  if (half) rope_kernel<TA, CD, D, true><<<grid, kRopeThreads, 0, s>>>(p, T, tokens);
+  else rope_kernel<TA, CD, D, false><<<grid, kRopeThreads, 0, s>>>(p, T, tokens);
   return cudaGetLastError();
 }
 
