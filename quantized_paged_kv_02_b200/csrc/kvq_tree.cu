@@ -200,9 +200,13 @@ kvq_status plan_tree(const Geometry& g, int batch, int num_q_heads, int max_tree
   p->kernel = tree_tc_supported(g, p->g) ? 1 : 0;
   p->ws_bytes = p->ws_ml_off = 0;
   p->splits = p->chunk = p->ctas = 0;
+  p->group = 1;
   if (p->kernel == 1) {
-    // two partial slots per CTA, each one tile of rows
-    p->ctas = sms;
+    // CTAs in groups of as many as a tree has row tiles, at most kTreeGroup; two partial slots per
+    // CTA, each one tile of rows
+    const long tiles = (static_cast<long>(max_tree) * p->g + kTreeRows - 1) / kTreeRows;
+    p->group = static_cast<int>(std::max(1L, std::min(tiles, static_cast<long>(std::min(kTreeGroup, sms)))));
+    p->ctas = sms / p->group * p->group;
     const size_t rows = static_cast<size_t>(2) * sms * kTreeRows;
     p->ws_ml_off = rows * g.D * sizeof(float);
     p->ws_bytes = p->ws_ml_off + rows * 2 * sizeof(float);
@@ -341,6 +345,7 @@ kvq_status kvq_tree_attention(const kvq_cache_desc* c, const void* q, int num_q_
   p.splits = plan.splits;
   p.chunk = plan.chunk;
   p.ctas = plan.ctas;
+  p.group = plan.group;
   p.fault = c->fault;
   const cudaError_t e = plan.kernel == 1 ? launch_tree_tc(p, g, stream) : launch_tree_simt(p, g.act_dtype, stream);
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

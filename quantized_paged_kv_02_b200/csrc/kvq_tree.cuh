@@ -7,6 +7,7 @@
 namespace kvq {
 
 constexpr int kTreeMax = 1024;       // drafted tokens per sequence at most
+constexpr int kTreeGroup = 4;        // CTAs that share a walk at most
 constexpr int kTreeRows = 128;       // tensor-core kernel: query rows per tile
 constexpr int kTreeBlk = 64;         // ... and cached tokens per block
 
@@ -15,6 +16,7 @@ struct TreePlan {
   int g;               // query heads per kv head
   int splits, chunk;   // kernel 0: token splits, tokens each
   int ctas;            // kernel 1: persistent CTAs
+  int group;           // ... of which this many walk the same blocks for different row tiles
   size_t ws_bytes, ws_ml_off;
 };
 
@@ -33,7 +35,7 @@ struct TreeParams {
   float scale_log2;
   void* out;
   int out_dtype;
-  int splits, chunk, ctas;
+  int splits, chunk, ctas, group;
   float* ws_o;
   float* ws_ml;
   int32_t* fault;
@@ -84,19 +86,27 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t* row, int pos, int 
   return w;
 }
 
-// Block-balanced schedule of the tensor-core kernel.  A unit is one (sequence, kv head, tile of
-// 128 query rows) and has ceil(n / 64) blocks; the blocks of all units, in the order
-// (sequence, kv head, tile), are cut into ctas contiguous ranges.  A CTA has at most two
-// segments that do not hold a whole unit: one that does not begin its unit (partial slot
-// 2 c) and one that begins but does not end it (slot 2 c + 1).
+// Block-balanced schedule of the tensor-core kernel.  A unit is one (sequence, kv head, row of
+// `group` tiles of 128 query rows) and has ceil(n / 64) blocks; the blocks of all units, in the
+// order (sequence, kv head, row of tiles), are cut into ctas / group contiguous ranges, one per
+// group of CTAs.  The CTAs of a group walk the same blocks at the same time, each for its own tile
+// of the row, so that the cache's bytes come from DRAM once for all of them (trees wider than one
+// tile; with tiles as units of their own the tiles of a sequence were read at different times, and
+// DRAM was the bound).  A CTA has at most two segments that do not hold a whole unit: one that
+// does not begin its unit (partial slot 2 c) and one that begins but does not end it (slot
+// 2 c + 1).
 __device__ __forceinline__ int tree_tiles(const TreeParams& p, int L) {
   return (L * p.g + kTreeRows - 1) / kTreeRows;
 }
+__device__ __forceinline__ int tree_tile_rows(const TreeParams& p, int L) {
+  return (tree_tiles(p, L) + p.group - 1) / p.group;
+}
 __device__ __forceinline__ int tree_blocks(int n) { return (n + kTreeBlk - 1) / kTreeBlk; }
 __device__ __forceinline__ long long tree_work(const TreeParams& p, const TreeSeq& s) {
-  return s.L > 0 ? static_cast<long long>(tree_tiles(p, s.L)) * p.H * tree_blocks(s.n) : 0;
+  return s.L > 0 ? static_cast<long long>(tree_tile_rows(p, s.L)) * p.H * tree_blocks(s.n) : 0;
 }
-__device__ __forceinline__ long long tree_range(long long W, int c, int C) { return W * c / C; }
+// First block of group k's range (k = the number of groups: the end).
+__device__ __forceinline__ long long tree_range(const TreeParams& p, long long W, int k) { return W * k / (p.ctas / p.group); }
 
 bool tree_tc_supported(const Geometry& g, int group);
 cudaError_t launch_tree_simt(const TreeParams& p, int act, cudaStream_t s);

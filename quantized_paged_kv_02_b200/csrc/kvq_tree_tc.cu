@@ -95,7 +95,7 @@ struct Seg {
 };
 
 struct Walk {
-  int b, u, j, tiles;
+  int b, u, j, tiles, rows;
   long long left;
   TreeSeq s;
   __device__ __forceinline__ void load(const TreeParams& p) {
@@ -105,6 +105,7 @@ struct Walk {
       ++b;
     }
     tiles = s.L > 0 ? tree_tiles(p, s.L) : 1;
+    rows = (tiles + p.group - 1) / p.group;
   }
   __device__ __forceinline__ Walk(const TreeParams& p, const int* sched) {
     b = sched[0];
@@ -113,26 +114,31 @@ struct Walk {
     left = sched[3];
     if (left > 0) load(p);
   }
+  // The next segment with a tile for this CTA (a short row of tiles has none for the last ones).
   __device__ __forceinline__ bool next(const TreeParams& p, Seg& g) {
-    if (left <= 0) return false;
-    if (u == p.H * tiles) {
-      u = 0;
-      ++b;
-      load(p);
+    while (left > 0) {
+      if (u == p.H * rows) {
+        u = 0;
+        ++b;
+        load(p);
+      }
+      g.kvh = u / rows;
+      g.tile = (u - g.kvh * rows) * p.group + blockIdx.x % p.group;
+      g.j0 = j;
+      g.nblk = tree_blocks(s.n);
+      g.j1 = static_cast<int>(min(static_cast<long long>(g.nblk), j + left));
+      left -= g.j1 - g.j0;
+      j = 0;
+      ++u;
+      if (g.tile < tiles) {
+        g.b = b;
+        g.q0 = s.q0;
+        g.L = s.L;
+        g.n = s.n;
+        return true;
+      }
     }
-    g.b = b;
-    g.kvh = u / tiles;
-    g.tile = u - g.kvh * tiles;
-    g.q0 = s.q0;
-    g.L = s.L;
-    g.n = s.n;
-    g.nblk = tree_blocks(s.n);
-    g.j0 = j;
-    g.j1 = static_cast<int>(min(static_cast<long long>(g.nblk), j + left));
-    left -= g.j1 - g.j0;
-    j = 0;
-    ++u;
-    return true;
+    return false;
   }
 };
 
@@ -391,7 +397,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
       W += w;
     }
-    const long long w0 = tree_range(W, blockIdx.x, p.ctas), w1 = tree_range(W, blockIdx.x + 1, p.ctas);
+    const int gr = blockIdx.x / p.group;
+    const long long w0 = tree_range(p, W, gr), w1 = tree_range(p, W, gr + 1);
     long long before = 0;
     int at_b = 0, at_u = 0, at_j = 0;
     for (int b0 = 0; b0 < p.B && w1 > w0; b0 += 32) {
@@ -1055,12 +1062,13 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p) {
   const int tok = i / p.Hq, hq = i - tok * p.Hq, kvh = hq / p.g;
   const int x = tok * p.g + hq - kvh * p.g, tile = x / kTreeRows, r = x - tile * kTreeRows;
   const int nblk = tree_blocks(s.n);
-  const long long U0 = before + (static_cast<long long>(kvh) * tree_tiles(p, s.L) + tile) * nblk, U1 = U0 + nblk;
-  // CTA c covers [W c / C, W (c + 1) / C): the last that starts at or before U0, and the last
+  const long long U0 = before + (static_cast<long long>(kvh) * tree_tile_rows(p, s.L) + tile / p.group) * nblk, U1 = U0 + nblk;
+  // group k covers [W k / K, W (k + 1) / K): the last that starts at or before U0, and the last
   // that starts before U1
-  const int c0 = static_cast<int>(((U0 + 1) * p.ctas + W - 1) / W) - 1, c1 = static_cast<int>((U1 * p.ctas + W - 1) / W) - 1;
+  const int K = p.ctas / p.group;
+  const int c0 = static_cast<int>(((U0 + 1) * K + W - 1) / W) - 1, c1 = static_cast<int>((U1 * K + W - 1) / W) - 1;
   if (c0 == c1) return;
-  // lane k describes CTA c0 + k; the partial rows are then read eight at a time, so that their
+  // lane k describes the CTA of group c0 + k; the partial rows are then read eight at a time, so that their
   // loads overlap
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1069,8 +1077,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p) {
     const int c = k0 + lane;
     long row = -1;
     float mk = -INFINITY, lk = 0.f;
-    if (c <= c1 && tree_range(W, c, p.ctas) < tree_range(W, c + 1, p.ctas)) {
-      row = (2L * c + (c == c0 ? 1 : 0)) * kTreeRows + r;
+    if (c <= c1 && tree_range(p, W, c) < tree_range(p, W, c + 1)) {
+      row = (2L * (c * p.group + tile % p.group) + (c == c0 ? 1 : 0)) * kTreeRows + r;
       const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * row);
       lk = v.y;
       if (lk != 0.f) mk = v.x;
