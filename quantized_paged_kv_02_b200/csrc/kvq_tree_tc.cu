@@ -50,7 +50,10 @@ constexpr int kSoftWarps = 8, kProdWarp = 8, kScoreWarp = 9, kConvWarp0 = 10, kO
 constexpr int kTile = 16384;         // K or V of a block: 64 x 128 16-bit elements
 constexpr int kQTile = 32768;        // 128 x 128
 constexpr int kNS = 4;               // score buffers: two per stream
-constexpr int kNQ = 8;               // slots of per-block scales and page flags
+// slots of per-block scales and page flags: the K converters write block J's once S of block J - 2
+// (16-bit caches: once P V of block J - 6) is complete, which came after P V of block J - 6, hence
+// after its softmax: the slot of block J - 8 is free
+constexpr int kNQ = 8;
 constexpr float kRebase = 8.f;       // log2 headroom before the running maximum is re-based
 // TMEM columns: scores / P of block J in [64 (J % 4), +64), O of stream s in [256 + 128 s, +128)
 constexpr uint32_t kTmemCols = 512, kTmO = 256;
@@ -82,8 +85,8 @@ struct Layout {
   static_assert(MISC_OFF % 16 == 0, "vmax is read four at a time");
   static_assert(!DIRECT || NBK == NBV, "16-bit caches fill K and V of a buffer together");
   // raw_full, raw_empty [RS]; tile_full [NBK] (DIRECT); k_full, k_free [NBK]; v_full, v_free
-  // [NBV]; s_full, s_free, p_full [kNS]; pv_done [2]; kq_full, kq_free [kNQ]; q_ready, o_full, sync, fin [2]
-  static constexpr int NBARS = 2 * RS + 3 * NBK + 2 * NBV + 3 * kNS + 2 + 2 * kNQ + 5;
+  // [NBV]; s_full, s_free, p_full [kNS]; pv_done [2]; q_ready, o_full, sync, fin [2]
+  static constexpr int NBARS = 2 * RS + 3 * NBK + 2 * NBV + 3 * kNS + 2 + 5;
   static constexpr int BYTES = 1024 + BAR_OFF + 8 * NBARS;
   static_assert(BYTES <= 227 * 1024, "fits the shared memory of one CTA");
   static_assert(BYTES > 114 * 1024, "one CTA per SM: its TMEM allocation never waits for a peer");
@@ -143,8 +146,8 @@ struct Walk {
 };
 
 struct Shared {
-  uint64_t *raw_full, *raw_empty, *tile_full, *k_full, *k_free, *v_full, *v_free, *s_full, *s_free, *p_full, *pv_done, *kq_full,
-      *kq_free, *q_ready, *o_full, *sync, *fin;
+  uint64_t *raw_full, *raw_empty, *tile_full, *k_full, *k_free, *v_full, *v_free, *s_full, *s_free, *p_full, *pv_done,
+      *q_ready, *o_full, *sync, *fin;
   int *pages, *pok, *snf, *vnf, *sched;
   float *vmax, *amax, *ks, *vs;
   uint32_t* tmem;
@@ -346,8 +349,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     sh.s_free = take(kNS);
     sh.p_full = take(kNS);
     sh.pv_done = take(2);
-    sh.kq_full = take(kNQ);
-    sh.kq_free = take(kNQ);
     sh.q_ready = take(1);
     sh.o_full = take(1);
     sh.sync = take(1);
@@ -368,15 +369,11 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       mbar_init(&sh.v_free[i], 1);
     }
     for (int i = 0; i < kNS; ++i) {
-      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_full[i], 2);
       mbar_init(&sh.s_free[i], 1);
       mbar_init(&sh.p_full[i], 4);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&sh.pv_done[i], 1);
-    for (int i = 0; i < kNQ; ++i) {
-      mbar_init(&sh.kq_full[i], 4);
-      mbar_init(&sh.kq_free[i], 4);
-    }
     mbar_init(sh.q_ready, kSoftWarps);
     mbar_init(sh.o_full, 1);
     mbar_init(sh.sync, kSoftWarps);
@@ -518,18 +515,16 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     const int c = ct & 15, rr = ct >> 4;
     bool run = true;
     const int nbuf = isv ? NBV : NBK;
-    int kb = 0, kround = 0, slot = 0, sround = 0, raw = 0, rround = 0;
+    int kb = 0, kround = 0, slot = 0, raw = 0, rround = 0;
     while (run && walk.next(p, sg)) {
       const int first = sg.n - sg.L;                          // first drafted position
       for (int j = sg.j0; j < sg.j1; ++j) {
         bool ok = true;
         if constexpr (DIRECT) {
-          if (!isv && sround > 0) ok = wait(&sh.kq_free[slot], (sround - 1) & 1, sh.abort);
-          if (ok) ok = wait(&sh.tile_full[kb], kround & 1, sh.abort);
+          ok = wait(&sh.tile_full[kb], kround & 1, sh.abort);
         } else {
           ok = wait(&sh.raw_full[raw], rround & 1, sh.abort);
           if (ok && kround > 0) ok = wait(isv ? &sh.v_free[kb] : &sh.k_free[kb], (kround - 1) & 1, sh.abort);
-          if (ok && !isv && sround > 0) ok = wait(&sh.kq_free[slot], (sround - 1) & 1, sh.abort);
         }
         run = __all_sync(0xffffffffu, ok);
         if (!run) break;
@@ -624,10 +619,9 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(isv ? &sh.v_full[kb] : &sh.k_full[kb]);
-          if (!isv) mbar_arrive(&sh.kq_full[slot]);
         }
         if (++kb == nbuf) { kb = 0; ++kround; }
-        if (++slot == kNQ) { slot = 0; ++sround; }
+        slot = (slot + 1) % kNQ;
         if (++raw == Y::RSD) { raw = 0; ++rround; }
       }
     }
@@ -645,7 +639,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       for (int j = sg.j0; j < sg.j1 && ok; ++j, ++J) {
         // the score buffer: P V of block J - 4 has read it
         bool fine = J < kNS || wait(&sh.s_free[J & 3], ((J >> 2) - 1) & 1, sh.abort);
-        if (fine) fine = wait(DIRECT ? &sh.tile_full[kb] : &sh.k_full[kb], kround & 1, sh.abort);
+        if (fine) fine = wait(&sh.k_full[kb], kround & 1, sh.abort);
+        if (DIRECT && fine) fine = wait(&sh.tile_full[kb], kround & 1, sh.abort);
         ok = __all_sync(0xffffffffu, fine);
         if (!ok) break;
         tc::fence_after_sync();
@@ -655,6 +650,9 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                      idS, kk > 0);
         commit_one(&sh.k_free[kb]);
         commit_one(&sh.s_full[J & 3]);
+        // (and this warp's own arrival: it hands on what it acquired from the K converters, the
+        // block's scales and page flags)
+        if (lane == 0) mbar_arrive(&sh.s_full[J & 3]);
         if (++kb == NBK) { kb = 0; ++kround; }
       }
       ++unit;
@@ -796,8 +794,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         if ((jj & 1) != st) continue;
         const int sb = jj & 3, slot = jj % kNQ;
         const uint32_t sbase = lanes + kTreeBlk * sb;
-        ok = wait(&sh.kq_full[slot], (jj / kNQ) & 1, sh.abort) && wait(&sh.s_full[sb], (jj >> 2) & 1, sh.abort);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, wait(&sh.s_full[sb], (jj >> 2) & 1, sh.abort));
         if (!ok) break;
         tc::fence_after_sync();
         const int pok = sh.pok[slot];
@@ -923,10 +920,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh.p_full[sb]);
-          mbar_arrive(&sh.kq_free[slot]);
-        }
+        if (lane == 0) mbar_arrive(&sh.p_full[sb]);
         if (!ok) break;
       }
       J += sg.j1 - sg.j0;
