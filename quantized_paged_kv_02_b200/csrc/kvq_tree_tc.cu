@@ -48,15 +48,15 @@ constexpr int kD = 128, kBS = 16, kPPB = kTreeBlk / kBS;
 constexpr int kThreads = 608;
 constexpr int kSoftWarps = 8, kProdWarp = 8, kScoreWarp = 9, kConvWarp0 = 10, kOutWarp = 18;
 constexpr int kTile = 16384;         // K or V of a block: 64 x 128 16-bit elements
-constexpr int kQTile = 32768;        // 128 x 128
-constexpr int kNS = 4;               // score buffers: two per stream
+constexpr int kNS = 3;               // score buffers: one in use per stream, one ahead
 // slots of per-block scales and page flags: the K converters write block J's once S of block J - 2
-// (16-bit caches: once P V of block J - 6) is complete, which came after P V of block J - 6, hence
-// after its softmax: the slot of block J - 8 is free
+// (16-bit caches: once P V of block J - 6) is complete, which came after P V of block J - 5 (J - 6),
+// hence after the softmax of all blocks up to that: the slot of block J - 8 is free
 constexpr int kNQ = 8;
 constexpr float kRebase = 8.f;       // log2 headroom before the running maximum is re-based
-// TMEM columns: scores / P of block J in [64 (J % 4), +64), O of stream s in [256 + 128 s, +128)
-constexpr uint32_t kTmemCols = 512, kTmO = 256;
+// TMEM columns: scores / P of block J in [64 (J % 3), +64), Q in [192, 256), O of stream s in
+// [256 + 128 s, +128)
+constexpr uint32_t kTmemCols = 512, kTmQ = 192, kTmO = 256;
 
 template <int CD, bool PT>
 struct Layout {
@@ -67,16 +67,16 @@ struct Layout {
   static constexpr int REC = OFF_S + (PT ? 8 * kBS : 0);
   // K and V tile buffers (a K tile is free once S has read it, a V tile only after P V), and the
   // raw ring of blocks (8-bit caches)
-  static constexpr int NBK = DIRECT ? 6 : 2, NBV = DIRECT ? 6 : 3;
-  static constexpr int RS = DIRECT ? 0 : 5;
+  static constexpr int NBK = DIRECT ? 6 : 2, NBV = DIRECT ? 6 : 4;
+  static constexpr int RS = DIRECT ? 0 : 6;
   static constexpr int RSD = RS > 0 ? RS : 1;                   // (a divisor)
   static constexpr int K_OFF = 0;
   static constexpr int V_OFF = NBK * kTile;
-  static constexpr int Q_OFF = V_OFF + NBV * kTile;
-  static constexpr int RAW_OFF = Q_OFF + kQTile;
+  static constexpr int RAW_OFF = V_OFF + NBV * kTile;
   static constexpr int KS_OFF = RAW_OFF + RS * kPPB * REC;      // float [kNQ][64] K scales (PT)
   static constexpr int VS_OFF = KS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [kNQ][64]: V scales
-  static constexpr int MISC_OFF = VS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);
+  static constexpr int EX_OFF = VS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [2][2][128], int [4]: a unit's end
+  static constexpr int MISC_OFF = EX_OFF + 4 * kTreeRows * 4 + 16;
   // vmax [kNQ][4]; nonfinite flags of scales [kNQ][4] and of V rows [NBV][4]; page masks of the raw
   // ring / tile buffers; pok [kNQ]; amax [8]; schedule [6]; tmem, abort
   static constexpr int NPOK = DIRECT ? NBK : RS;
@@ -187,12 +187,6 @@ __device__ __forceinline__ uint64_t first_mnmajor(uint32_t tile) { return tc::sm
 
 // One thread of the warp issues (the operands stay in the warp's uniform registers, which a
 // branch on the lane would take them out of).
-__device__ __forceinline__ void mma_ss_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u) : "memory");
-}
 __device__ __forceinline__ void mma_ts_one(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -631,14 +625,14 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     // (the whole warp runs the loop, so that descriptors stay in uniform registers)
     const uint32_t tiles = smem_u32(smem);
     constexpr uint32_t idS = tc::idesc_f16(BF, false, kTreeRows, kTreeBlk);
-    const uint64_t dq = first_kmajor(tiles + Y::Q_OFF), dk = first_kmajor(tiles + Y::K_OFF);
+    const uint64_t dk = first_kmajor(tiles + Y::K_OFF);
     bool ok = true;
-    int unit = 0, kb = 0, kround = 0;
+    int unit = 0, kb = 0, kround = 0, sb = 0, sround = 0;
     while (ok && walk.next(p, sg)) {
       ok = __all_sync(0xffffffffu, wait(sh.q_ready, unit & 1, sh.abort));
       for (int j = sg.j0; j < sg.j1 && ok; ++j, ++J) {
-        // the score buffer: P V of block J - 4 has read it
-        bool fine = J < kNS || wait(&sh.s_free[J & 3], ((J >> 2) - 1) & 1, sh.abort);
+        // the score buffer: P V of block J - 3 has read it
+        bool fine = sround == 0 || wait(&sh.s_free[sb], (sround - 1) & 1, sh.abort);
         if (fine) fine = wait(&sh.k_full[kb], kround & 1, sh.abort);
         if (DIRECT && fine) fine = wait(&sh.tile_full[kb], kround & 1, sh.abort);
         ok = __all_sync(0xffffffffu, fine);
@@ -646,14 +640,14 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         tc::fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ss_one(tbase + kTreeBlk * (J & 3), dq + step_kmajor<kTreeRows>(kk), dk + kb * (kTile / 16) + step_kmajor<kTreeBlk>(kk),
-                     idS, kk > 0);
+          mma_ts_one(tbase + kTreeBlk * sb, tbase + kTmQ + 8 * kk, dk + kb * (kTile / 16) + step_kmajor<kTreeBlk>(kk), idS, kk > 0);
         commit_one(&sh.k_free[kb]);
-        commit_one(&sh.s_full[J & 3]);
+        commit_one(&sh.s_full[sb]);
         // (and this warp's own arrival: it hands on what it acquired from the K converters, the
         // block's scales and page flags)
-        if (lane == 0) mbar_arrive(&sh.s_full[J & 3]);
+        if (lane == 0) mbar_arrive(&sh.s_full[sb]);
         if (++kb == NBK) { kb = 0; ++kround; }
+        if (++sb == kNS) { sb = 0; ++sround; }
       }
       ++unit;
     }
@@ -667,12 +661,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     constexpr uint32_t idPV = tc::idesc_f16(BF, true, kTreeRows, kD);
     const uint64_t dv = first_mnmajor(smem_u32(smem) + Y::V_OFF);
     bool ok = true;
-    int vb = 0, vround = 0;
+    int vb = 0, vround = 0, sb = 0, sround = 0;
     while (ok && walk.next(p, sg)) {
       for (int j = sg.j0; j < sg.j1 && ok; ++j, ++J) {
         const int st = J & 1;
         bool fine = wait(&sh.v_full[vb], vround & 1, sh.abort);
-        if (fine) fine = wait(&sh.p_full[J & 3], (J >> 2) & 1, sh.abort);
+        if (fine) fine = wait(&sh.p_full[sb], sround & 1, sh.abort);
         ok = __all_sync(0xffffffffu, fine);
         if (!ok) break;
         tc::fence_after_sync();
@@ -680,13 +674,14 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         for (int pa = 0; pa < (HILO ? 2 : 1); ++pa)
 #pragma unroll
           for (int kk = 0; kk < kTreeBlk / 16; ++kk)
-            mma_ts_one(tbase + kTmO + 128 * st, tbase + kTreeBlk * (J & 3) + 16 * kk + 8 * pa, dv + vb * (kTile / 16) + kk * 128,
+            mma_ts_one(tbase + kTmO + 128 * st, tbase + kTreeBlk * sb + 16 * kk + 8 * pa, dv + vb * (kTile / 16) + kk * 128,
                        idPV, j > sg.j0 + 1 || pa > 0 || kk > 0);
         commit_one(&sh.v_free[vb]);
-        commit_one(&sh.s_free[J & 3]);
+        commit_one(&sh.s_free[sb]);
         commit_one(&sh.pv_done[st]);
         if (j == sg.j1 - 1) commit_one(sh.o_full);
         if (++vb == NBV) { vb = 0; ++vround; }
+        if (++sb == kNS) { sb = 0; ++sround; }
       }
     }
     if (!ok && lane == 0) fail(p, sh.abort);
@@ -699,7 +694,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     const int r = 32 * quarter + lane;                        // row of the tile (TMEM lane)
     const uint32_t lanes = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t obase = lanes + kTmO + 128 * st;
-    float* ex = reinterpret_cast<float*>(smem + Y::Q_OFF);    // [2][2][128] at a unit's end
+    float* ex = reinterpret_cast<float*>(smem + Y::EX_OFF);   // [2][2][128] at a unit's end
     int* exf = reinterpret_cast<int*>(ex + 512);              // [2] nonfinite drafted rows seen
     int unit = 0, syncs = 0, seen = 0;                        // seen: blocks of this stream
     bool ok = true;
@@ -712,23 +707,20 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     };
     while (ok && walk.next(p, sg)) {
       const int R = sg.L * p.g - sg.tile * kTreeRows;         // rows of the tile that exist
-      // --- q rows -> the Q tile (16 rows per warp, 16 lanes per row)
+      const int x = sg.tile * kTreeRows + r;
+      const bool row_ok = r < R, warp_ok = 32 * quarter < R;
+      const int tok = row_ok ? x / p.g : 0;
+      const long orow = (static_cast<long>(sg.q0) + tok) * p.Hq + static_cast<long>(sg.kvh) * p.g + (x - tok * p.g);
+      // --- this row's q, channels [64 st, 64 st + 64), to tensor memory
       float qsc = p.scale_log2;
       {
         if (p.mode == KVQ_SCALE_PER_HEAD) qsc *= p.k_static[sg.kvh];
         if (p.mode == KVQ_SCALE_PER_TENSOR) qsc *= p.k_static[0];
-        const int c = lane & 15;
         uint4 u[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rq = warp * 16 + 2 * i + (lane >> 4);
-          u[i] = make_uint4(0, 0, 0, 0);
-          if (rq < R) {
-            const int x = sg.tile * kTreeRows + rq, tok = x / p.g;
-            const long row = (static_cast<long>(sg.q0) + tok) * p.Hq + static_cast<long>(sg.kvh) * p.g + (x - tok * p.g);
-            u[i] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * kD)[c];
-          }
-        }
+        for (int i = 0; i < 8; ++i)
+          u[i] = row_ok ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow * kD + 64 * st)[i]
+                        : make_uint4(0, 0, 0, 0);
         if constexpr (!BF) {
           if (!p.act_fp16) {
             // bf16 activations in fp16 tiles: the tile's largest |q| sets a power of two that
@@ -736,10 +728,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
             float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              float x[8];
-              unpack8<__nv_bfloat16>(u[i], x);
+              float v[8];
+              unpack8<__nv_bfloat16>(u[i], v);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -755,31 +747,26 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
             qsc = ldexpf(qsc, eq);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              float x[8];
-              unpack8<__nv_bfloat16>(u[i], x);
-              u[i] = make_uint4(pack_f16x2(x[0] * down, x[1] * down), pack_f16x2(x[2] * down, x[3] * down),
-                                pack_f16x2(x[4] * down, x[5] * down), pack_f16x2(x[6] * down, x[7] * down));
+              float v[8];
+              unpack8<__nv_bfloat16>(u[i], v);
+              u[i] = make_uint4(pack_f16x2(v[0] * down, v[1] * down), pack_f16x2(v[2] * down, v[3] * down),
+                                pack_f16x2(v[4] * down, v[5] * down), pack_f16x2(v[6] * down, v[7] * down));
             }
           }
         }
-        if (qsc < 0.f) {                                      // a negative static scale: in q's sign
-          qsc = -qsc;
+        const uint32_t flip = qsc < 0.f ? 0x80008000u : 0u;   // a negative static scale: in q's sign
+        qsc = fabsf(qsc);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) (&u[i].x)[e] ^= 0x80008000u;
-          }
+        for (int i = 0; i < 8; i += 2) {
+          const uint32_t w[8] = {u[i].x ^ flip, u[i].y ^ flip, u[i].z ^ flip, u[i].w ^ flip,
+                                 u[i + 1].x ^ flip, u[i + 1].y ^ flip, u[i + 1].z ^ flip, u[i + 1].w ^ flip};
+          st8(lanes + kTmQ + 32 * st + 4 * i, w);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(smem + Y::Q_OFF + tile_off<kTreeRows>(warp * 16 + 2 * i + (lane >> 4), c)) = u[i];
-        tc::fence_async_shared();
+        tc::st_wait();
+        tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(sh.q_ready);
       }
-      const int x = sg.tile * kTreeRows + r;
-      const bool row_ok = r < R, warp_ok = 32 * quarter < R;
-      const int tok = row_ok ? x / p.g : 0;
       const uint32_t* mrow = p.mask + (static_cast<long>(sg.q0) + tok) * p.mask_words;
       const int first = sg.n - sg.L;
       // Running maximum m, an integer, raised to the next one above a score that exceeds it by
@@ -792,9 +779,9 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       for (int j = sg.j0; j < sg.j1; ++j) {
         const int jj = J + j - sg.j0;
         if ((jj & 1) != st) continue;
-        const int sb = jj & 3, slot = jj % kNQ;
+        const int sb = jj % kNS, slot = jj % kNQ;
         const uint32_t sbase = lanes + kTreeBlk * sb;
-        ok = __all_sync(0xffffffffu, wait(&sh.s_full[sb], (jj >> 2) & 1, sh.abort));
+        ok = __all_sync(0xffffffffu, wait(&sh.s_full[sb], (jj / kNS) & 1, sh.abort));
         if (!ok) break;
         tc::fence_after_sync();
         const int pok = sh.pok[slot];
@@ -925,9 +912,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       }
       J += sg.j1 - sg.j0;
       if (!ok) break;
-      // --- the unit's end: both streams' (offset, sum) through shared memory (the Q tile is
-      // free: every MMA of the unit is complete), then stream st joins the two accumulators
-      // for output channels [64 st, 64 st + 64)
+      // --- the unit's end: both streams' (offset, sum) through shared memory, then stream st joins
+      // the two accumulators for output channels [64 st, 64 st + 64)
       ok = __all_sync(0xffffffffu, wait(sh.o_full, unit & 1, sh.abort));
       ++unit;
       if (!ok) break;
@@ -953,7 +939,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       if (p.mode == KVQ_SCALE_PER_TENSOR) vmul = p.v_static[0];
       const float mul = whole ? (lt != 0.f ? vmul / lt : 0.f) : vmul;
       const long prow = (2L * blockIdx.x + (sg.j0 == 0 ? 1 : 0)) * kTreeRows + r;    // partial row
-      const long orow = (static_cast<long>(sg.q0) + tok) * p.Hq + static_cast<long>(sg.kvh) * p.g + (x - tok * p.g);
       if (!whole && st == 0 && row_ok) *reinterpret_cast<float2*>(p.ws_ml + 2 * prow) = make_float2(off, lt);
       if (warp_ok) {
 #pragma unroll 1
@@ -1017,7 +1002,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         }
       }
       tc::fence_before_sync();
-      // every warp has read the accumulators and the exchange area before the next unit's Q
+      // every warp has read the accumulators and the exchange area before the next unit begins
       ok = sync8();
     }
     if (!ok && lane == 0) fail(p, sh.abort);
