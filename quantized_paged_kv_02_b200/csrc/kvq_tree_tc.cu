@@ -355,7 +355,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     }
     for (int i = 0; i < NBK; ++i) {
       mbar_init(&sh.tile_full[i], 1);
-      mbar_init(&sh.k_full[i], 4);
+      mbar_init(&sh.k_full[i], DIRECT ? 1 : 4);
       mbar_init(&sh.k_free[i], 1);
     }
     for (int i = 0; i < NBV; ++i) {
@@ -434,8 +434,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
   Seg sg;
   int J = 0;                                                  // blocks of the CTA so far
 
-  if (warp == kProdWarp) {
+  if (warp == kProdWarp || (DIRECT && warp >= kConvWarp0 && warp < kConvWarp0 + 3)) {
     // ------------------------------------------------------------ producer
+    // 16-bit caches: four warps, each with one of a page's four copies (K and V, two column halves:
+    // a tensor copy takes about a hundred cycles to issue, and one warp issuing all sixteen of a
+    // block was the bound); the first also announces the bytes and sends for what comes next
+    const int part = warp == kProdWarp ? 0 : warp - kConvWarp0 + 1;
     bool run = true;
     int buf = 0, round = 0;                                   // of the raw ring / the tiles
     constexpr int RING = DIRECT ? NBK : Y::RSD;
@@ -453,13 +457,13 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
           cur = next;
           const int k = j * kPPB + 32 + lane;
           next = k < stop ? table[k] : -1;
-        } else if (at == 2 && next >= 0 && next < p.NB) {
+        } else if (at == 2 && part == 0 && next >= 0 && next < p.NB) {
           prefetch_l2(p.pages + (static_cast<long>(next) * p.H + sg.kvh) * Y::REC, Y::REC);
         }
         const int blk = __shfl_sync(0xffffffffu, cur, at * kPPB + (lane & (kPPB - 1)));
         const bool mine = lane < kPPB && j * kPPB + lane < stop;
         const bool valid = mine && blk >= 0 && blk < p.NB;
-        if (mine && !valid) record_fault(p.fault, KVQ_FAULT_BLOCK);
+        if (mine && !valid && part == 0) record_fault(p.fault, KVQ_FAULT_BLOCK);
         const unsigned vm = __ballot_sync(0xffffffffu, valid);
         bool ok = true;
         if (lane == 0 && round > 0) {
@@ -471,20 +475,18 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         run = __all_sync(0xffffffffu, ok);
         if (!run) break;
         uint64_t* full = DIRECT ? &sh.tile_full[buf] : &sh.raw_full[buf];
-        if (lane == 0) {
+        if (lane == 0 && part == 0) {
           sh.pages[buf] = static_cast<int>(vm);
           mbar_arrive_expect_tx(full, __popc(vm) * Y::REC);
         }
         __syncwarp();
         if (valid) {
           if constexpr (DIRECT) {
-            // 16 K rows and 16 V rows of 256 bytes, as two 128-byte halves each
-            const int y = (blk * p.H + sg.kvh) * (2 * kBS), r0 = lane * kBS * 128;
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              tma_load_2d(smem + Y::K_OFF + buf * kTile + hh * (kTile / 2) + r0, &rows, full, 128 * hh, y);
-              tma_load_2d(smem + Y::V_OFF + buf * kTile + hh * (kTile / 2) + r0, &rows, full, 128 * hh, y + kBS);
-            }
+            // 16 rows of K (parts 0, 1) or V (2, 3), one 128-byte half of their 256 bytes.  (A part
+            // may be ahead of the announcement: the phase still waits for that one arrival.)
+            const int y = (blk * p.H + sg.kvh) * (2 * kBS) + (part >> 1) * kBS, hh = part & 1;
+            tma_load_2d(smem + (part >> 1 ? Y::V_OFF : Y::K_OFF) + buf * kTile + hh * (kTile / 2) + lane * kBS * 128, &rows, full,
+                        128 * hh, y);
           } else {
             bulk_load(smem + Y::RAW_OFF + (buf * kPPB + lane) * Y::REC,
                       p.pages + (static_cast<long>(blk) * p.H + sg.kvh) * Y::REC, Y::REC, full);
@@ -494,8 +496,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       }
     }
     if (!run && lane == 0) fail(p, sh.abort);
-    // every copy issued must land before the CTA may exit
-    if (lane == 0) {
+    // every copy issued must land before the CTA may exit (the first part's wait covers all parts)
+    if (lane == 0 && part == 0) {
       for (int i = max(0, J - RING); i < J; ++i)
         if (!mbar_drain(DIRECT ? &sh.tile_full[i % RING] : &sh.raw_full[i % RING], (i / RING) & 1))
           record_fault(p.fault, KVQ_FAULT_TIMEOUT);
@@ -504,6 +506,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     // ------------------------------------------------------------ converters
     // thread (c, rr): 16-byte chunk c of rows rr and rr + 8 of every page; K: thread ct < 64 also
     // carries token ct's scales; 16-bit caches, V: token ct's zeros
+    // (16-bit caches: K's fourth warp alone hands on the page flags)
     const bool isv = warp >= kConvWarp0 + 4;
     const int cw = (warp - kConvWarp0) & 3, ct = cw * 32 + lane;
     const int c = ct & 15, rr = ct >> 4;
@@ -608,7 +611,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
           nf = __any_sync(0xffffffffu, nf);
           if (lane == 0) sh.vnf[kb * 4 + cw] = nf;
         }
-        if (!isv && ct == 0) sh.pok[slot] = pok;
+        if (!isv && (DIRECT ? lane == 0 : ct == 0)) sh.pok[slot] = pok;
         tc::fence_async_shared();
         __syncwarp();
         if (lane == 0) {
