@@ -53,7 +53,8 @@ constexpr int kNS = 3;               // score buffers: one in use per stream, on
 // (16-bit caches: once P V of block J - 6) is complete, which came after P V of block J - 5 (J - 6),
 // hence after the softmax of all blocks up to that: the slot of block J - 8 is free
 constexpr int kNQ = 8;
-constexpr float kRebase = 8.f;       // log2 headroom before the running maximum is re-based
+constexpr float kRebase = 8.f;       // log2 headroom before the running maximum is re-based,
+constexpr float kMostSum = 8192.f;   // or the sum of 32 weights that asks for it
 // TMEM columns: scores / P of block J in [64 (J % 3), +64), Q in [192, 256), O of stream s in
 // [256 + 128 s, +128)
 constexpr uint32_t kTmemCols = 512, kTmQ = 192, kTmO = 256;
@@ -772,16 +773,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       }
       const uint32_t* mrow = p.mask + (static_cast<long>(sg.q0) + tok) * p.mask_words;
       const int first = sg.n - sg.L;
-      // Running maximum m, an integer, raised to the next one above a score that exceeds it by
-      // 2^8, so that every factor between two maxima is a power of two and re-basing is exact;
-      // ev the exponent of the largest V scale so far.  P holds e = 2^(x - off), off = m + ev, times
-      // the token's V scale, below 2^10; l and O accumulate in that domain.
+      // m: an integer near the running maximum, raised when weights grow past 2^8 .. 2^13, so that
+      // every factor between two of its values is a power of two and re-basing is exact; ev the
+      // exponent of the largest V scale so far.  P holds e = 2^(x - off), off = m + ev, times the
+      // token's V scale, below 2^14; l and O accumulate in that domain.
       float m = -INFINITY, moff = 0.f, l = 0.f;               // moff: m, or 0 before the first score
       int ev = 0, nfseen = 0;                                 // (PT)
       bool begun = false;
-      for (int j = sg.j0; j < sg.j1; ++j) {
-        const int jj = J + j - sg.j0;
-        if ((jj & 1) != st) continue;
+      for (int jj = J + ((J ^ st) & 1); jj < J + sg.j1 - sg.j0; jj += 2) {
+        const int j = sg.j0 + jj - J;
         const int sb = jj % kNS, slot = jj % kNQ;
         const uint32_t sbase = lanes + kTreeBlk * sb;
         ok = __all_sync(0xffffffffu, wait(&sh.s_full[sb], (jj / kNS) & 1, sh.abort));
@@ -821,68 +821,80 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
           }
           const float2 q2 = make_float2(qsc, qsc);
           float2 lsum = make_float2(0.f, 0.f);
-          // --- one pass, 32 columns at a time: scores times the K scale, their maximum, e, its sum,
-          // and P over the scores it came from
+          const float most = PT ? kMostSum * pow2i(-ev) : kMostSum;
+          // m raised to the next integer above mx for the lanes that ask: l and O (and P of the block's
+          // columns before column c0) into the new domain
+          auto rebase = [&](bool ask, float mx, int c0) {
+            float f = 1.f;
+            if (ask) {
+              const float mn = ceilf(mx);
+              f = m == -INFINITY ? 0.f : pow2i(static_cast<int>(fmaxf(m - mn, -1000.f)));
+              m = moff = mn;
+            }
+            l *= f;
+            lsum = __fmul2_rn(lsum, make_float2(f, f));
+            tc::st_wait();
+            if (begun) {
+              settle();
+              scale_f32(obase, 8, f);
+            }
+            scale_p<BF, HILO>(sbase, c0 / 16, f);
+          };
+          // --- 32 columns at a time: scores times the K scale, e, its sum, and P over the scores
+          // they came from
           auto block = [&](auto masked) {
+            constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll 1
             for (int cc = 0; cc < kTreeBlk / 32; ++cc) {
               uint32_t s[32];
-              tc::ld32(sbase + 32 * cc, s);
               float2 t[16];
+              auto load = [&]() {
+                tc::ld32(sbase + 32 * cc, s);
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                t[i] = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-                t[i + 1] = make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3]));
-                if constexpr (PT) {
-                  const float4 f = *reinterpret_cast<const float4*>(ks + 32 * cc + 2 * i);
-                  t[i] = __fmul2_rn(t[i], make_float2(f.x, f.y));
-                  t[i + 1] = __fmul2_rn(t[i + 1], make_float2(f.z, f.w));
+                for (int i = 0; i < 16; i += 2) {
+                  t[i] = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+                  t[i + 1] = make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3]));
+                  if constexpr (PT) {
+                    const float4 f = *reinterpret_cast<const float4*>(ks + 32 * cc + 2 * i);
+                    t[i] = __fmul2_rn(t[i], make_float2(f.x, f.y));
+                    t[i + 1] = __fmul2_rn(t[i + 1], make_float2(f.z, f.w));
+                  }
                 }
-              }
-              if constexpr (decltype(masked)::value) {
+              };
+              auto largest = [&]() {
+                float m0 = fmaxf(t[0].x, t[0].y), m1 = fmaxf(t[1].x, t[1].y);
+#pragma unroll
+                for (int i = 2; i < 16; i += 2) {
+                  m0 = max3(m0, t[i].x, t[i].y);
+                  m1 = max3(m1, t[i + 1].x, t[i + 1].y);
+                }
+                return fmaxf(m0, m1) * qsc;
+              };
+              load();
+              if constexpr (MASKED) {
                 const uint32_t vis = column_bits(mrow, pok, j, cc, sg.n, sg.L);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   if (!((vis >> (2 * i)) & 1u)) t[i].x = -INFINITY;
                   if (!((vis >> (2 * i + 1)) & 1u)) t[i].y = -INFINITY;
                 }
+                const float mx = largest();
+                const bool ask = mx > m + kRebase;
+                if (__any_sync(0xffffffffu, ask)) rebase(ask, mx, 32 * cc);
               }
-              float m0 = fmaxf(t[0].x, t[0].y), m1 = fmaxf(t[1].x, t[1].y);
+              uint32_t ph[16], pl[HILO ? 16 : 1];
+              auto weights = [&]() {
+                const float off = PT ? moff + static_cast<float>(ev) : moff;
+                const float2 noff = make_float2(-off, -off);
+                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int i = 2; i < 16; i += 2) {
-                m0 = max3(m0, t[i].x, t[i].y);
-                m1 = max3(m1, t[i + 1].x, t[i + 1].y);
-              }
-              const float mx = fmaxf(m0, m1) * qsc;
-              if (__any_sync(0xffffffffu, mx > m + kRebase)) {
-                float f = 1.f;
-                if (mx > m + kRebase) {
-                  const float mn = ceilf(mx);
-                  f = m == -INFINITY ? 0.f : pow2i(static_cast<int>(fmaxf(m - mn, -1000.f)));
-                  m = moff = mn;
-                }
-                l *= f;
-                lsum = __fmul2_rn(lsum, make_float2(f, f));
-                tc::st_wait();
-                if (begun) {
-                  settle();
-                  scale_f32(obase, 8, f);
-                }
-                scale_p<BF, HILO>(sbase, 2 * cc, f);
-              }
-              const float off = PT ? moff + static_cast<float>(ev) : moff;
-              const float2 noff = make_float2(-off, -off);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t ph[8], pl[8];
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                  float2 a = __ffma2_rn(t[8 * h + i], q2, noff), b = __ffma2_rn(t[8 * h + i + 1], q2, noff);
+                for (int i = 0; i < 16; i += 2) {
+                  float2 a = __ffma2_rn(t[i], q2, noff), b = __ffma2_rn(t[i + 1], q2, noff);
                   a = make_float2(ex2(a.x), ex2(a.y));
                   b = make_float2(ex2(b.x), ex2(b.y));
-                  lsum = __fadd2_rn(lsum, __fadd2_rn(a, b));
+                  sum = __fadd2_rn(sum, __fadd2_rn(a, b));
                   if constexpr (PT) {
-                    const float4 f = *reinterpret_cast<const float4*>(vsp + 32 * cc + 16 * h + 2 * i);
+                    const float4 f = *reinterpret_cast<const float4*>(vsp + 32 * cc + 2 * i);
                     a = __fmul2_rn(a, make_float2(f.x, f.y));
                     b = __fmul2_rn(b, make_float2(f.z, f.w));
                   }
@@ -894,10 +906,27 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                     ph[i + 1] = pack2<BF>(b);
                   }
                 }
-                st8(sbase + 32 * cc + 16 * h, ph);
-                if constexpr (HILO) st8(sbase + 32 * cc + 16 * h + 8, pl);
-                else (void)pl;
+                return sum;
+              };
+              float2 sum = weights();
+              if constexpr (!MASKED) {
+                // every column is visible: the maximum need not be known as long as the 32 weights (less
+                // their 2^-ev) sum to no more than 2^13: P then stays inside fp16.  It is found, from
+                // the scores again, for a row's first columns and when that fails.
+                const bool ask = sum.x + sum.y > most || m == -INFINITY;
+                if (__any_sync(0xffffffffu, ask)) {
+                  load();
+                  rebase(ask, largest(), 32 * cc);
+                  sum = weights();
+                }
               }
+              lsum = __fadd2_rn(lsum, sum);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                st8(sbase + 32 * cc + 16 * h, ph + 8 * h);
+                if constexpr (HILO) st8(sbase + 32 * cc + 16 * h + 8, pl + 8 * h);
+              }
+              (void)pl;
             }
           };
           if (fast) block(std::false_type{});
