@@ -76,7 +76,8 @@ struct Layout {
   static constexpr int RAW_OFF = V_OFF + NBV * kTile;
   static constexpr int KS_OFF = RAW_OFF + RS * kPPB * REC;      // float [kNQ][64] K scales (PT)
   static constexpr int VS_OFF = KS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [kNQ][64]: V scales
-  static constexpr int EX_OFF = VS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [2][2][128], int [4]: a unit's end
+  static constexpr int KQ_OFF = VS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [8][64]: a softmax warp's score factors (PT)
+  static constexpr int EX_OFF = KQ_OFF + (PT ? kSoftWarps * kTreeBlk * 4 : 0);   // float [2][2][128], int [4]: a unit's end
   static constexpr int MISC_OFF = EX_OFF + 4 * kTreeRows * 4 + 16;
   // vmax [kNQ][4]; nonfinite flags of scales [kNQ][4] and of V rows [NBV][4]; page masks of the raw
   // ring / tile buffers; pok [kNQ]; amax [8]; schedule [6]; tmem, abort
@@ -802,7 +803,17 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
           tc::fence_after_sync();
         };
         if (warp_ok) {
-          const float* ks = sh.ks + slot * kTreeBlk;
+          float* kq = reinterpret_cast<float*>(smem + Y::KQ_OFF) + warp * kTreeBlk;
+          if constexpr (PT) {
+            // each token's score factor, once for the warp's 32 rows: K scale times the tile's
+            const float2 f = reinterpret_cast<const float2*>(sh.ks + slot * kTreeBlk)[lane];
+            __syncwarp();                                     // (the block before has been read)
+            reinterpret_cast<float2*>(kq)[lane] = make_float2(f.x * qsc, f.y * qsc);
+            __syncwarp();
+          }
+          auto factor = [&](int c) {
+            return PT ? *reinterpret_cast<const float4*>(kq + c) : make_float4(qsc, qsc, qsc, qsc);
+          };
           const float* vsp = sh.vs + slot * kTreeBlk;
           if constexpr (PT) {
             const float2 v2 = *reinterpret_cast<const float2*>(sh.vmax + slot * 4);
@@ -819,7 +830,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
               scale_f32(obase, 8, f);
             }
           }
-          const float2 q2 = make_float2(qsc, qsc);
           float2 lsum = make_float2(0.f, 0.f);
           const float most = PT ? kMostSum * pow2i(-ev) : kMostSum;
           // m raised to the next integer above mx for the lanes that ask: l and O (and P of the block's
@@ -848,17 +858,14 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
             for (int cc = 0; cc < kTreeBlk / 32; ++cc) {
               uint32_t s[32];
               float2 t[16];
+              // the scores of the 32 columns in the exponent's units
               auto load = [&]() {
                 tc::ld32(sbase + 32 * cc, s);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                  t[i] = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-                  t[i + 1] = make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3]));
-                  if constexpr (PT) {
-                    const float4 f = *reinterpret_cast<const float4*>(ks + 32 * cc + 2 * i);
-                    t[i] = __fmul2_rn(t[i], make_float2(f.x, f.y));
-                    t[i + 1] = __fmul2_rn(t[i + 1], make_float2(f.z, f.w));
-                  }
+                  const float4 f = factor(32 * cc + 2 * i);
+                  t[i] = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f.x, f.y));
+                  t[i + 1] = __fmul2_rn(make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3])), make_float2(f.z, f.w));
                 }
               };
               auto largest = [&]() {
@@ -868,10 +875,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                   m0 = max3(m0, t[i].x, t[i].y);
                   m1 = max3(m1, t[i + 1].x, t[i + 1].y);
                 }
-                return fmaxf(m0, m1) * qsc;
+                return fmaxf(m0, m1);
               };
-              load();
-              if constexpr (MASKED) {
+              if constexpr (!MASKED) {
+                tc::ld32(sbase + 32 * cc, s);
+              } else {
+                load();
                 const uint32_t vis = column_bits(mrow, pok, j, cc, sg.n, sg.L);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -889,7 +898,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                  float2 a = __ffma2_rn(t[i], q2, noff), b = __ffma2_rn(t[i + 1], q2, noff);
+                  float2 a, b;
+                  if constexpr (MASKED) {
+                    a = __fadd2_rn(t[i], noff);
+                    b = __fadd2_rn(t[i + 1], noff);
+                  } else {
+                    const float4 f = factor(32 * cc + 2 * i);
+                    a = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f.x, f.y), noff);
+                    b = __ffma2_rn(make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3])), make_float2(f.z, f.w), noff);
+                  }
                   a = make_float2(ex2(a.x), ex2(a.y));
                   b = make_float2(ex2(b.x), ex2(b.y));
                   sum = __fadd2_rn(sum, __fadd2_rn(a, b));
