@@ -278,10 +278,22 @@ def kvq_read_device_fault(desc, reset=True, stream=None):
 
 # The wrappers below run once per layer and step beside kernels of a few microseconds, so they
 # look at each tensor once and hand the addresses over as plain integers.
-def _raw_stream(stream):
+def _here():
+    """The current device, which the call runs on and every tensor has to be on."""
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream
+
+
+def _at(t, dev, what):
+    """Address of a tensor on device dev (a host address, or another device's, would fault)."""
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, not on the current device" % (what, t.device))
+    return t.data_ptr()
 
 
 def _rows(t, what):
@@ -298,13 +310,13 @@ def _rows(t, what):
     return T, H, D, a if T > 1 else H * D
 
 
-def _index(t, n, what):
+def _index(t, n, dev, what):
     """Address of an index tensor of n entries (contiguous int32)."""
     if t.dtype != torch.int32 or not t.is_contiguous():
         raise TypeError("%s must be contiguous int32" % what)
     if t.numel() != n:
         raise ValueError("%s must have %d entries, got %d" % (what, n, t.numel()))
-    return t.data_ptr()
+    return _at(t, dev, what)
 
 
 _ACT_CODE = {torch.bfloat16: 0, torch.float16: 1}
@@ -325,6 +337,7 @@ def kvq_rope(rope, freqs, positions, q=None, k=None, q_out=None, k_out=None, str
     act = q.dtype if q is not None else k.dtype
     if act not in _ACT_CODE:
         raise TypeError("activations must be bfloat16 or float16, got %s" % act)
+    dev = _here()
     T = D = None
     args = []
     for x, out, what in ((q, q_out, "q"), (k, k_out, "k")):
@@ -346,13 +359,13 @@ def kvq_rope(rope, freqs, positions, q=None, k=None, q_out=None, k_out=None, str
             os = shape[3]
         if x.dtype != act or out.dtype != act:
             raise TypeError("q, k and their outputs must have one type")
-        args += (x.data_ptr(), xs, H, out.data_ptr(), os)
+        args += (_at(x, dev, what), xs, H, _at(out, dev, what), os)
         if x is q:
             q_out = out
         else:
             k_out = out
-    st = lib.kvq_rope(ctypes.byref(rope), freqs.data_ptr(), _ACT_CODE[act], D, _index(positions, T, "positions"), T, *args,
-                      _raw_stream(stream))
+    st = lib.kvq_rope(ctypes.byref(rope), _at(freqs, dev, "freqs"), _ACT_CODE[act], D, _index(positions, T, dev, "positions"), T,
+                      *args, _raw_stream(stream, dev))
     if st:
         _check(st, "kvq_rope")
     return (q_out if q is not None else None), (k_out if k is not None else None)
@@ -368,6 +381,7 @@ def kvq_rope_write(desc, rope, freqs, positions, q, k_new, v_new, slot_mapping, 
         raise TypeError("k_new and v_new must have the cache's activation type")
     if Tv != T or H != desc.num_kv_heads or Hv != H or D != desc.head_dim or Dv != D:
         raise ValueError("k_new and v_new must be [tokens, %d, %d]" % (desc.num_kv_heads, desc.head_dim))
+    dev = _here()
     qp, qs, hq, qop, qos = None, 0, 0, None, 0
     if q is not None:
         Tq, hq, Dq, qs = _rows(q, "q")
@@ -382,10 +396,11 @@ def kvq_rope_write(desc, rope, freqs, positions, q, k_new, v_new, slot_mapping, 
                 raise ValueError("q_out must have the shape of q")
         if q.dtype != act or q_out.dtype != act:
             raise TypeError("q and q_out must have the cache's activation type")
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-    st = lib.kvq_rope_write(ctypes.byref(desc), ctypes.byref(rope), freqs.data_ptr(), _index(positions, T, "positions"), T,
-                            qp, qs, hq, qop, qos, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-                            _index(slot_mapping, T, "slot_mapping"), _raw_stream(stream))
+        qp, qop = _at(q, dev, "q"), _at(q_out, dev, "q_out")
+    st = lib.kvq_rope_write(ctypes.byref(desc), ctypes.byref(rope), _at(freqs, dev, "freqs"),
+                            _index(positions, T, dev, "positions"), T, qp, qs, hq, qop, qos, _at(k_new, dev, "k_new"), ks,
+                            _at(v_new, dev, "v_new"), vs, _index(slot_mapping, T, dev, "slot_mapping"),
+                            _raw_stream(stream, dev))
     if st:
         _check(st, "kvq_rope_write")
     return q_out
@@ -399,7 +414,9 @@ def kvq_gather(desc, slots, k_out, v_out, stream=None):
             raise ValueError("%s must be contiguous [%d, %d, %d]" % (what, n, desc.num_kv_heads, desc.head_dim))
         if _ACT_CODE.get(t.dtype) != desc.act_dtype:
             raise TypeError("%s must have the cache's activation type" % what)
-    st = lib.kvq_gather(ctypes.byref(desc), _index(slots, n, "slots"), n, k_out.data_ptr(), v_out.data_ptr(), _raw_stream(stream))
+    dev = _here()
+    st = lib.kvq_gather(ctypes.byref(desc), _index(slots, n, dev, "slots"), n, _at(k_out, dev, "k_out"), _at(v_out, dev, "v_out"),
+                        _raw_stream(stream, dev))
     if st:
         _check(st, "kvq_gather")
     return k_out, v_out
@@ -426,14 +443,15 @@ def kvq_tree_attention(desc, q, q_start, max_tree, tree_mask, block_tables, cont
     if tree_mask.dim() != 2 or block_tables.dim() != 2:
         raise ValueError("tree_mask must be [tokens, words] and block_tables [batch, blocks]")
     words, blocks = tree_mask.shape[1], block_tables.shape[1]
+    dev = _here()
     ws, ws_bytes = None, 0
     if workspace is not None:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = _at(workspace, dev, "workspace"), workspace.numel() * workspace.element_size()
     st = lib.kvq_tree_attention(
-        ctypes.byref(desc), q.data_ptr(), T, B, Hq, _index(q_start, B + 1, "q_start"), max_tree,
-        _index(tree_mask, T * words, "tree_mask"), words, _index(block_tables, B * blocks, "block_tables"), blocks,
-        _index(context_lens, B, "context_lens"), max_context, softmax_scale, out.data_ptr(), _OUT_CODE[out.dtype], ws, ws_bytes,
-        _raw_stream(stream))
+        ctypes.byref(desc), _at(q, dev, "q"), T, B, Hq, _index(q_start, B + 1, dev, "q_start"), max_tree,
+        _index(tree_mask, T * words, dev, "tree_mask"), words, _index(block_tables, B * blocks, dev, "block_tables"), blocks,
+        _index(context_lens, B, dev, "context_lens"), max_context, softmax_scale, _at(out, dev, "out"), _OUT_CODE[out.dtype],
+        ws, ws_bytes, _raw_stream(stream, dev))
     if st:
         _check(st, "kvq_tree_attention")
     return out
@@ -446,11 +464,12 @@ def kvq_tree_commit(desc, path, accepted, q_start, block_tables, context_lens, n
     if path.dim() != 2 or block_tables.dim() != 2:
         raise ValueError("path must be [batch, accepted at most] and block_tables [batch, blocks]")
     most, blocks = path.shape[1], block_tables.shape[1]
+    dev = _here()
     st = lib.kvq_tree_commit(
-        ctypes.byref(desc), _index(path, B * most, "path"), most, _index(accepted, B, "accepted"), B,
-        _index(q_start, B + 1, "q_start"), _index(block_tables, B * blocks, "block_tables"), blocks,
-        _index(context_lens, B, "context_lens"), None if new_lens is None else _index(new_lens, B, "new_lens"),
-        _raw_stream(stream))
+        ctypes.byref(desc), _index(path, B * most, dev, "path"), most, _index(accepted, B, dev, "accepted"), B,
+        _index(q_start, B + 1, dev, "q_start"), _index(block_tables, B * blocks, dev, "block_tables"), blocks,
+        _index(context_lens, B, dev, "context_lens"), None if new_lens is None else _index(new_lens, B, dev, "new_lens"),
+        _raw_stream(stream, dev))
     if st:
         _check(st, "kvq_tree_commit")
     return new_lens

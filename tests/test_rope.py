@@ -240,6 +240,9 @@ def test_rope_wrapper_checks():
         r.apply(pos, q, q_out=q[:, :1])
     with pytest.raises(TypeError):
         r.apply(pos, q.float())
+    for bad in ((pos.cpu(), q), (pos, q.cpu())):                    # host tensors
+        with pytest.raises(ValueError):
+            r.apply(*bad)
 
 
 def _cache(cd, act, mode, nb, bs, H, D, seed=0):

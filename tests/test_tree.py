@@ -210,6 +210,32 @@ def test_outlier_channels():
 
 
 @gpu
+@pytest.mark.parametrize("cd,mode,act", [("int8", "per_token_head", "bf16"), ("fp8", "per_head", "fp16"), ("bf16", "none", "bf16")])
+@pytest.mark.parametrize("step", [0.3, 4.0])
+def test_scores_that_keep_growing(cd, mode, act, step):
+    """Keys along the query's direction, longer with every position: each block holds a new maximum, by a
+    little or by many powers of two, so that the running maximum is re-based in visible blocks."""
+    n, L, D = 700, 4, 128
+    w, q, starts, sees, mask, most = make(cd, mode, act, 4, 1, D, 16, [n], [L], seed=3)
+    d = torch.randn(D, generator=torch.Generator().manual_seed(9))
+    d = d / d.norm()
+    q = (q.float() * 0.02 + 4.0 * d).to(q.dtype)
+    grow = torch.arange(n).float()[:, None, None] * step / 64
+    w.k = (w.k.float() * 0.05 + grow * d).to(w.k.dtype)
+    w.v = (w.v.float() * (1 + torch.arange(n).float()[:, None, None] / 100)).to(w.v.dtype)     # V scales grow too
+    static = None if mode != "per_head" else ([0.25], [0.125])
+    oc, gc = helpers.oracle_cache(w, static), helpers.gpu_cache(w, static=static)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    for od in (F32, B16):
+        check(run(gc, w, q, starts, mask, most, od), want, spread, od)
+    # and shrinking: the maximum comes first
+    w.k, w.v = w.k.flip(0).contiguous(), w.v.flip(0).contiguous()
+    oc, gc = helpers.oracle_cache(w, static), helpers.gpu_cache(w, static=static)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    check(run(gc, w, q, starts, mask, most), want, spread, F32)
+
+
+@gpu
 def test_many_short_sequences_and_one_long():
     """Several units per CTA, and one unit cut into hundreds of parts."""
     lens = [1 + 7 * (i % 40) for i in range(200)] + [20000]
@@ -393,3 +419,7 @@ def test_wrapper_checks():
     for bad in (dict(tree_mask=a["tree_mask"].long()), dict(q_start=a["q_start"].long())):
         with pytest.raises(TypeError):
             gc.tree_attention(**{**a, **bad})
+    # a host tensor is refused, not dereferenced
+    for name in ("q", "q_start", "tree_mask", "block_tables", "context_lens"):
+        with pytest.raises(ValueError):
+            gc.tree_attention(**{**a, name: a[name].cpu(), "out": torch.empty_like(a["q"])})
