@@ -6,7 +6,7 @@ exponent, at most about 60 for these inputs), so it is off by at most 128 * 2^-2
 which moves the result by no more than 2 * 5e-4 * ln 2 of spread = sum w |v| / sum w; the
 weights' own rounding (two halves: 2^-16 at worst) adds less than 2^-15 of it.  Together
 below 2^-10 spread.  bf16 output rounds once more (eps / 2 = 2^-8 of the result, half a step
-at most) and, for 8-bit and fp16 caches, weights of 11 bits (2^-12 of spread, inside the 2^-10).
+at most) and, for 8-bit and fp16 caches, weights of 11 bits (2^-11 of spread, inside the 2^-10).
 """
 
 import ctypes
@@ -231,6 +231,49 @@ def test_scores_that_keep_growing(cd, mode, act, step):
     # and shrinking: the maximum comes first
     w.k, w.v = w.k.flip(0).contiguous(), w.v.flip(0).contiguous()
     oc, gc = helpers.oracle_cache(w, static), helpers.gpu_cache(w, static=static)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    check(run(gc, w, q, starts, mask, most), want, spread, F32)
+
+
+@gpu
+@pytest.mark.parametrize("cd,mode,act", [("int8", "per_token_head", "fp16"), ("fp8", "per_head", "bf16"), ("bf16", "none", "bf16")])
+@pytest.mark.parametrize("up", [12.0, 60.0, 400.0])
+def test_one_position_far_above_the_rest(cd, mode, act, up):
+    """One visible position whose score is `up` powers of two above all before it: its weight relative to
+    the running maximum overflows a half (12), or binary32 (400: scores of 2^8 carry an error of
+    128 * 2^-24 * 400 = 2^-8.4, but then no other weight is above 2^-300 and the result is that V row)."""
+    n, L, D = 500, 3, 128
+    w, q, starts, sees, mask, most = make(cd, mode, act, 4, 1, D, 16, [n], [L], seed=4)
+    d = torch.randn(D, generator=torch.Generator().manual_seed(9)).sign() / D ** 0.5
+    q = (q.float() * 0.01 + 8.0 * d).to(q.dtype)
+    w.k = (w.k.float() * 0.05).to(w.k.dtype)
+    w.k[333] += (d * (up / (8.0 * 1.4426950408889634) * D ** 0.5)).to(w.k.dtype)
+    static = None if mode != "per_head" else ([0.0625], [0.03125])
+    oc, gc = helpers.oracle_cache(w, static), helpers.gpu_cache(w, static=static)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    for od in (F32, B16):
+        check(run(gc, w, q, starts, mask, most, od), want, spread, od)
+
+
+@gpu
+def test_largest_trees():
+    """1024 drafted tokens, once without any prefix: 64 tiles of rows per head, walked by groups of CTAs,
+    beside a sequence whose last tile row has one tile."""
+    w, q, starts, sees, mask, most = make("int8", "per_token_head", "bf16", 16, 2, 128, 16, [1024, 1500, 300], [1024, 1024, 70],
+                                          noise=True)
+    oc, gc = helpers.oracle_cache(w), helpers.gpu_cache(w)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    got = run(gc, w, q, starts, mask, most)
+    check(got, want, spread, F32)
+    assert torch.equal(got, run(gc, w, q, starts, mask, most))
+
+
+@gpu
+def test_sequences_that_share_pages():
+    """Two sequences with one prefix in the same pages."""
+    w, q, starts, sees, mask, most = make("fp8", "per_token_head", "bf16", 8, 2, 128, 16, [300, 300], [12, 12])
+    w.block_tables[1, :18] = w.block_tables[0, :18]
+    oc, gc = helpers.oracle_cache(w), helpers.gpu_cache(w)
     want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
     check(run(gc, w, q, starts, mask, most), want, spread, F32)
 
