@@ -10,6 +10,7 @@ constexpr int kTreeMax = 1024;       // drafted tokens per sequence at most
 constexpr int kTreeGroup = 4;        // CTAs that share a walk at most
 constexpr int kTreeRows = 128;       // tensor-core kernel: query rows per tile
 constexpr int kTreeBlk = 64;         // ... and cached tokens per block
+constexpr int kTreeLead = 6;         // a unit's start and end take as long as this many blocks
 
 struct TreePlan {
   int kernel;          // 0 CUDA cores, 1 tensor cores (tcgen05)
@@ -17,6 +18,7 @@ struct TreePlan {
   int splits, chunk;   // kernel 0: token splits, tokens each
   int ctas;            // kernel 1: persistent CTAs
   int group;           // ... of which this many walk the same blocks for different row tiles
+  int lead;            // ... and what a unit's start and end weigh, in blocks
   size_t ws_bytes, ws_ml_off;
 };
 
@@ -35,7 +37,7 @@ struct TreeParams {
   float scale_log2;
   void* out;
   int out_dtype;
-  int splits, chunk, ctas, group;
+  int splits, chunk, ctas, group, lead;
   float* ws_o;
   float* ws_ml;
   int32_t* fault;
@@ -102,11 +104,30 @@ __device__ __forceinline__ int tree_tile_rows(const TreeParams& p, int L) {
   return (tree_tiles(p, L) + p.group - 1) / p.group;
 }
 __device__ __forceinline__ int tree_blocks(int n) { return (n + kTreeBlk - 1) / kTreeBlk; }
-__device__ __forceinline__ long long tree_work(const TreeParams& p, const TreeSeq& s) {
-  return s.L > 0 ? static_cast<long long>(tree_tile_rows(p, s.L)) * p.H * tree_blocks(s.n) : 0;
+// A unit weighs its blocks and `lead` more, for its start and end.
+__device__ __forceinline__ unsigned tree_work(const TreeParams& p, const TreeSeq& s) {
+  return s.L > 0 ? static_cast<unsigned>(tree_tile_rows(p, s.L) * p.H) * (tree_blocks(s.n) + p.lead) : 0;
 }
-// First block of group k's range (k = the number of groups: the end).
-__device__ __forceinline__ long long tree_range(const TreeParams& p, long long W, int k) { return W * k / (p.ctas / p.group); }
+// The cut of W into ctas / group shares: the first `more` of them have `each` + 1, the others `each`.
+// (32 bits: the entry point refuses calls that could pass 2^31; 64-bit divisions are a kilobyte of code
+// apiece, which a small call waits for.)
+struct TreeCut {
+  unsigned each, more;
+};
+__device__ __forceinline__ TreeCut tree_cut(const TreeParams& p, unsigned W) {
+  const unsigned K = p.ctas / p.group;
+  TreeCut c;
+  c.each = W / K;
+  c.more = W - c.each * K;
+  return c;
+}
+// Start of share k.
+__device__ __forceinline__ unsigned tree_start(const TreeCut& c, unsigned k) { return c.each * k + min(k, c.more); }
+// The share that holds position u.
+__device__ __forceinline__ int tree_share(const TreeCut& c, unsigned u) {
+  const unsigned head = c.more * (c.each + 1);
+  return static_cast<int>(u < head ? u / (c.each + 1) : c.more + (u - head) / max(c.each, 1u));
+}
 
 bool tree_tc_supported(const Geometry& g, int group);
 cudaError_t launch_tree_simt(const TreeParams& p, int act, cudaStream_t s);

@@ -78,7 +78,8 @@ struct Layout {
   static constexpr int VS_OFF = KS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [kNQ][64]: V scales
   static constexpr int KQ_OFF = VS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [8][64]: a softmax warp's score factors (PT)
   static constexpr int EX_OFF = KQ_OFF + (PT ? kSoftWarps * kTreeBlk * 4 : 0);   // float [2][2][128], int [4]: a unit's end
-  static constexpr int MISC_OFF = EX_OFF + 4 * kTreeRows * 4 + 16;
+  static constexpr int WALK_OFF = EX_OFF + 4 * kTreeRows * 4 + 16;        // Walk [warps]
+  static constexpr int MISC_OFF = WALK_OFF + (kThreads / 32 + 1) / 2 * 128;
   // vmax [kNQ][4]; nonfinite flags of scales [kNQ][4] and of V rows [NBV][4]; page masks of the raw
   // ring / tile buffers; pok [kNQ]; amax [8]; schedule [6]; tmem, abort
   static constexpr int NPOK = DIRECT ? NBK : RS;
@@ -99,53 +100,49 @@ struct Seg {
   int b, kvh, tile, q0, L, n, nblk, j0, j1;
 };
 
+// A warp's place in the schedule, in shared memory; walk_next is a function of its own, since seven
+// copies of it kept the loops of the roles from sharing the instruction cache.
 struct Walk {
-  int b, u, j, tiles, rows;
-  long long left;
-  TreeSeq s;
-  __device__ __forceinline__ void load(const TreeParams& p) {
-    while (b < p.B) {
-      s = tree_seq(p, b);
-      if (s.L > 0) break;
-      ++b;
-    }
-    tiles = s.L > 0 ? tree_tiles(p, s.L) : 1;
-    rows = (tiles + p.group - 1) / p.group;
-  }
-  __device__ __forceinline__ Walk(const TreeParams& p, const int* sched) {
-    b = sched[0];
-    u = sched[1];
-    j = sched[2];
-    left = sched[3];
-    if (left > 0) load(p);
-  }
-  // The next segment with a tile for this CTA (a short row of tiles has none for the last ones).
-  __device__ __forceinline__ bool next(const TreeParams& p, Seg& g) {
-    while (left > 0) {
-      if (u == p.H * rows) {
-        u = 0;
-        ++b;
-        load(p);
-      }
-      g.kvh = u / rows;
-      g.tile = (u - g.kvh * rows) * p.group + blockIdx.x % p.group;
-      g.j0 = j;
-      g.nblk = tree_blocks(s.n);
-      g.j1 = static_cast<int>(min(static_cast<long long>(g.nblk), j + left));
-      left -= g.j1 - g.j0;
-      j = 0;
-      ++u;
-      if (g.tile < tiles) {
-        g.b = b;
-        g.q0 = s.q0;
-        g.L = s.L;
-        g.n = s.n;
-        return true;
-      }
-    }
-    return false;
-  }
+  Seg g;                                                      // the segment walk_next found
+  int b, u, pos;                                              // where the next begins; pos: in the unit, its lead included
+  int left;
 };
+
+// The next segment with a tile for this CTA (a short row of tiles has none for the last ones); the
+// whole warp calls.
+__device__ __noinline__ bool walk_next(const TreeParams& p, Walk* walk) {
+  __syncwarp();
+  Walk w = *walk;
+  __syncwarp();
+  bool found = false;
+  while (w.left > 0 && !found) {
+    const TreeSeq s = w.b < p.B ? tree_seq(p, w.b) : TreeSeq{0, 0, 0};
+    const int tiles = tree_tiles(p, s.L), rows = tree_tile_rows(p, s.L);
+    if (w.b >= p.B) break;
+    if (w.u >= p.H * rows) {
+      w.u = 0;
+      ++w.b;
+      continue;
+    }
+    w.g.kvh = w.u / rows;
+    w.g.tile = (w.u - w.g.kvh * rows) * p.group + blockIdx.x % p.group;
+    w.g.nblk = tree_blocks(s.n);
+    const int take = min(p.lead + w.g.nblk - w.pos, w.left);
+    w.g.j0 = max(w.pos - p.lead, 0);
+    w.g.j1 = w.pos + take - p.lead;
+    w.left -= take;
+    w.pos = 0;
+    ++w.u;
+    found = w.g.j1 > w.g.j0 && w.g.tile < tiles;
+    w.g.b = w.b;
+    w.g.q0 = s.q0;
+    w.g.L = s.L;
+    w.g.n = s.n;
+  }
+  if ((threadIdx.x & 31) == 0) *walk = w;
+  __syncwarp();
+  return found;
+}
 
 struct Shared {
   uint64_t *raw_full, *raw_empty, *tile_full, *k_full, *k_free, *v_full, *v_free, *s_full, *s_free, *p_full, *pv_done,
@@ -159,10 +156,10 @@ struct Shared {
 // Bounded wait that also gives up when another role has; the thread sleeps in the barrier.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
+  const uint32_t t0 = static_cast<uint32_t>(clock());
   while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
     if (*abort) return false;
-    if (clock64() - t0 > kWaitCycles) return false;
+    if (static_cast<uint32_t>(clock()) - t0 > static_cast<uint32_t>(kWaitCycles)) return false;
   }
   return true;
 }
@@ -252,6 +249,10 @@ __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
 // Bring a page record into L2 (a hint: it completes on its own and faults nothing).
 __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_line(const void* src) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
 }
 
 // O or P columns [base, base + 16 n) of the warp's lanes times a power of two per lane: float32
@@ -353,15 +354,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
   if (threadIdx.x == 0) {
     for (int i = 0; i < Y::RS; ++i) {
       mbar_init(&sh.raw_full[i], 1);
-      mbar_init(&sh.raw_empty[i], 8);
+      mbar_init(&sh.raw_empty[i], 4);
     }
     for (int i = 0; i < NBK; ++i) {
       mbar_init(&sh.tile_full[i], 1);
-      mbar_init(&sh.k_full[i], DIRECT ? 1 : 4);
+      mbar_init(&sh.k_full[i], DIRECT ? 1 : 2);
       mbar_init(&sh.k_free[i], 1);
     }
     for (int i = 0; i < NBV; ++i) {
-      mbar_init(&sh.v_full[i], 4);
+      mbar_init(&sh.v_full[i], DIRECT ? 4 : 2);
       mbar_init(&sh.v_free[i], 1);
     }
     for (int i = 0; i < kNS; ++i) {
@@ -375,6 +376,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     mbar_init(sh.sync, kSoftWarps);
     mbar_init(&sh.fin[0], 1);
     mbar_init(&sh.fin[1], 1);
+    for (int i = 0; i < 4 * NBV; ++i) sh.vnf[i] = 0;
     *sh.abort = 0;
     fence_mbar_init();
   }
@@ -383,40 +385,32 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
   griddep_wait();
   if (warp == 0) {
     // this CTA's share of the blocks, and the unit it begins in
-    long long W = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      long long w = b0 + lane < p.B ? tree_work(p, tree_seq(p, b0 + lane, blockIdx.x == 0)) : 0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-      W += w;
-    }
-    const int gr = blockIdx.x / p.group;
-    const long long w0 = tree_range(p, W, gr), w1 = tree_range(p, W, gr + 1);
-    long long before = 0;
-    int at_b = 0, at_u = 0, at_j = 0;
+    unsigned W = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += 32)
+      W += __reduce_add_sync(0xffffffffu, b0 + lane < p.B ? tree_work(p, tree_seq(p, b0 + lane, blockIdx.x == 0)) : 0);
+    const TreeCut cut = tree_cut(p, W);
+    const unsigned w0 = tree_start(cut, blockIdx.x / p.group), w1 = tree_start(cut, blockIdx.x / p.group + 1);
+    unsigned before = 0;
+    int at_b = 0, at_u = 0, at_pos = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B && w1 > w0; b0 += 32) {
       const bool have = b0 + lane < p.B;
       const TreeSeq s = have ? tree_seq(p, b0 + lane) : TreeSeq{0, 0, 0};
-      const long long w = have ? tree_work(p, s) : 0;
-      long long sum = w;                                      // inclusive prefix
-#pragma unroll
+      const unsigned w = have ? tree_work(p, s) : 0;
+      unsigned sum = w;                                       // inclusive prefix
+#pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, sum, o);
+        const unsigned t = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += t;
       }
-      const bool mine = w > 0 && before + sum - w <= w0 && w0 < before + sum;
-      if (mine) {
-        const int in = static_cast<int>(w0 - (before + sum - w)), nblk = tree_blocks(s.n);
-        at_b = b0 + lane;
-        at_u = in / nblk;
-        at_j = in - at_u * nblk;
-      }
+      const bool mine = before + sum - w <= w0 && w0 < before + sum;
       const unsigned m = __ballot_sync(0xffffffffu, mine);
       if (m) {
-        const int src = __ffs(m) - 1;
-        at_b = __shfl_sync(0xffffffffu, at_b, src);
-        at_u = __shfl_sync(0xffffffffu, at_u, src);
-        at_j = __shfl_sync(0xffffffffu, at_j, src);
+        const unsigned in = w0 - (before + sum - w), unit = tree_blocks(s.n) + p.lead;
+        at_b = b0 + __ffs(m) - 1;
+        at_u = __shfl_sync(0xffffffffu, in / max(unit, 1u), __ffs(m) - 1);
+        at_pos = __shfl_sync(0xffffffffu, in % max(unit, 1u), __ffs(m) - 1);
         break;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
@@ -424,7 +418,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     if (lane == 0) {
       sh.sched[0] = at_b;
       sh.sched[1] = at_u;
-      sh.sched[2] = at_j;
+      sh.sched[2] = at_pos;
       sh.sched[3] = static_cast<int>(w1 - w0);
     }
   }
@@ -432,8 +426,19 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tbase = *sh.tmem;
-  Walk walk(p, sh.sched);
+  Walk* walk = reinterpret_cast<Walk*>(smem + Y::WALK_OFF) + warp;
+  if (lane == 0) {
+    walk->b = sh.sched[0];
+    walk->u = sh.sched[1];
+    walk->pos = sh.sched[2];
+    walk->left = sh.sched[3];
+  }
   Seg sg;
+  auto next_segment = [&]() {
+    const bool more = walk_next(p, walk);
+    sg = walk->g;
+    return more;
+  };
   int J = 0;                                                  // blocks of the CTA so far
 
   if (warp == kProdWarp || (DIRECT && warp >= kConvWarp0 && warp < kConvWarp0 + 3)) {
@@ -445,7 +450,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     bool run = true;
     int buf = 0, round = 0;                                   // of the raw ring / the tiles
     constexpr int RING = DIRECT ? NBK : Y::RSD;
-    while (run && walk.next(p, sg)) {
+    while (run && next_segment()) {
       const int npg = (sg.n + kBS - 1) / kBS;
       // table entries 32 pages (8 blocks) at a time, one per lane, the next 32 loaded while these
       // are used and their pages sent for into L2 (a block's own entries, read when it is due,
@@ -453,6 +458,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       const int32_t* table = p.tables + static_cast<long>(sg.b) * p.max_blocks;
       const int base = sg.j0 * kPPB, stop = min(sg.j1 * kPPB, npg);
       int cur = -1, next = base + lane < stop ? table[base + lane] : -1;
+      if (part == 0) {
+        // the unit's q and mask rows, which softmax needs some blocks from now
+        const int x0 = sg.tile * kTreeRows, x1 = min(x0 + kTreeRows, sg.L * p.g) - 1;
+        for (int t = x0 / p.g + lane; t <= x1 / p.g; t += 32) {
+          const long row = static_cast<long>(sg.q0) + t;
+          prefetch_l2(static_cast<const uint16_t*>(p.q) + (row * p.Hq + static_cast<long>(sg.kvh) * p.g) * kD, p.g * kD * 2);
+          prefetch_line(p.mask + row * p.mask_words);
+        }
+      }
       for (int j = sg.j0; j < sg.j1 && run; ++j, ++J) {
         const int at = (j - sg.j0) & 7;                       // block of the batch
         if (at == 0) {
@@ -506,24 +520,33 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     }
   } else if (warp >= kConvWarp0 && warp < kOutWarp) {
     // ------------------------------------------------------------ converters
-    // thread (c, rr): 16-byte chunk c of rows rr and rr + 8 of every page; K: thread ct < 64 also
-    // carries token ct's scales; 16-bit caches, V: token ct's zeros
-    // (16-bit caches: K's fourth warp alone hands on the page flags)
+    // 8-bit caches: two warps per block and tensor (four for every block spent more on what each block
+    // costs a warp than on its codes): thread (c, rr) has 16-byte chunk c of rows rr + 4 k of every page;
+    // K: thread ct also carries token ct's scales.  16-bit caches, V: token ct's zeros, and K's fourth
+    // warp alone hands on the page flags
     const bool isv = warp >= kConvWarp0 + 4;
-    const int cw = (warp - kConvWarp0) & 3, ct = cw * 32 + lane;
+    const int cw = (warp - kConvWarp0) & 3, ct = (DIRECT ? cw : cw & 1) * 32 + lane;
     const int c = ct & 15, rr = ct >> 4;
+    constexpr int kStep = DIRECT ? 1 : 2;
     bool run = true;
-    const int nbuf = isv ? NBV : NBK;
-    int kb = 0, kround = 0, slot = 0, raw = 0, rround = 0;
-    while (run && walk.next(p, sg)) {
+    int at = DIRECT ? 0 : cw >> 1;                            // this warp's next block of the CTA
+    int raw = at, rpar = 0, kb = 0, kpar = 0;
+    while (run && next_segment()) {
       const int first = sg.n - sg.L;                          // first drafted position
-      for (int j = sg.j0; j < sg.j1; ++j) {
+      const int end = J + sg.j1 - sg.j0;
+      for (; at < end; at += kStep) {
+        const int j = sg.j0 + at - J;
+        if constexpr (!DIRECT) {
+          kb = at & ((isv ? NBV : NBK) - 1);
+          kpar = isv ? at / NBV : at / NBK;
+        }
+        const int slot = at & (kNQ - 1);
         bool ok = true;
         if constexpr (DIRECT) {
-          ok = wait(&sh.tile_full[kb], kround & 1, sh.abort);
+          ok = wait(&sh.tile_full[kb], kpar & 1, sh.abort);
         } else {
-          ok = wait(&sh.raw_full[raw], rround & 1, sh.abort);
-          if (ok && kround > 0) ok = wait(isv ? &sh.v_free[kb] : &sh.k_free[kb], (kround - 1) & 1, sh.abort);
+          ok = wait(&sh.raw_full[raw], rpar, sh.abort);
+          if (ok && kpar > 0) ok = wait(isv ? &sh.v_free[kb] : &sh.k_free[kb], (kpar - 1) & 1, sh.abort);
         }
         run = __all_sync(0xffffffffu, ok);
         if (!run) break;
@@ -537,7 +560,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
             const bool keep = pos < sg.n && ((pok >> (ct / kBS)) & 1);
             uint8_t* tile = smem + Y::V_OFF + kb * kTile;
             if (!keep || pos >= first) {
-#pragma unroll 4
+#pragma unroll 1
               for (int cc = 0; cc < 16; ++cc) {
                 uint4* a = reinterpret_cast<uint4*>(tile + tile_off<kTreeBlk>(ct, cc));
                 uint4 u = keep ? *a : make_uint4(0, 0, 0, 0);
@@ -548,17 +571,19 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
             }
           }
         } else {
-          uint8_t* tile = smem + (isv ? Y::V_OFF : Y::K_OFF) + kb * kTile + tile_off<kTreeBlk>(rr, c) - rr * 128;
+          uint8_t* tile = smem + (isv ? Y::V_OFF : Y::K_OFF) + kb * kTile;
+          uint8_t* even = tile + tile_off<kTreeBlk>(rr, c);        // rows rr + 8 i, and
+          uint8_t* odd = tile + tile_off<kTreeBlk>(rr + 4, c);     // rr + 4 + 8 i
           const uint8_t* src = smem + Y::RAW_OFF + raw * (kPPB * Y::REC);
           const uint8_t* row = src + (isv ? Y::OFF_V : 0) + rr * Y::ROWB + 8 * c;
-          uint2 w[kPPB][2];
+          uint2 w[kPPB][4];
 #pragma unroll
           for (int pp = 0; pp < kPPB; ++pp)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) w[pp][k] = *reinterpret_cast<const uint2*>(row + pp * Y::REC + 8 * k * Y::ROWB);
+            for (int k = 0; k < 4; ++k) w[pp][k] = *reinterpret_cast<const uint2*>(row + pp * Y::REC + 4 * k * Y::ROWB);
           float kscale = 0.f, vscale = 0.f;
           if constexpr (PT) {
-            if (!isv && ct < kTreeBlk) {
+            if (!isv) {
               const float* sc = reinterpret_cast<const float*>(src + (ct >> 4) * Y::REC + Y::OFF_S) + (ct & 15);
               kscale = sc[0];
               vscale = sc[kBS];
@@ -566,27 +591,33 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.raw_empty[raw]);
+          raw += 2;
+          if (raw >= Y::RS) { raw -= Y::RS; rpar ^= 1; }
           auto code16 = [&](const uint2& x) { return CD == KVQ_DTYPE_INT8 ? i8x8_to_f16(x) : e4m3x8_to_f16(x); };
-          if (whole) {
 #pragma unroll
-            for (int pp = 0; pp < kPPB; ++pp)
+          for (int pp = 0; pp < kPPB; ++pp)
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                *reinterpret_cast<uint4*>(tile + (pp * kBS + rr + 8 * k) * 128) = code16(w[pp][k]);
-          } else {
-#pragma unroll
-            for (int pp = 0; pp < kPPB; ++pp)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int t = pp * kBS + rr + 8 * k, pos = j * kTreeBlk + t;
-                uint4 u = code16(w[pp][k]);
-                if (!(((pok >> pp) & 1) && pos < sg.n)) u = make_uint4(0, 0, 0, 0);
-                else if (CD == KVQ_DTYPE_FP8_E4M3 && isv && pos >= first) nf = drop_nonfinite<false>(u) || nf;
-                *reinterpret_cast<uint4*>(tile + t * 128) = u;
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>((k & 1 ? odd : even) + (pp * kBS + 8 * (k >> 1)) * 128) = code16(w[pp][k]);
+          if (!whole) {
+            // rows that are not there to zeros, and drafted V without its infinities and NaN
+#pragma unroll 1
+            for (int i = 0; i < 4 * kPPB; ++i) {
+              const int t = 4 * i + rr, pos = j * kTreeBlk + t;
+              uint4* a = reinterpret_cast<uint4*>(tile + tile_off<kTreeBlk>(t, c));
+              if (!(((pok >> (i >> 2)) & 1) && pos < sg.n)) {
+                *a = make_uint4(0, 0, 0, 0);
+              } else if (CD == KVQ_DTYPE_FP8_E4M3 && isv && pos >= first) {
+                uint4 u = *a;
+                if (drop_nonfinite<false>(u)) {
+                  *a = u;
+                  nf = true;
+                }
               }
+            }
           }
           if constexpr (PT) {
-            if (!isv && ct < kTreeBlk) {                       // whole warps
+            if (!isv) {
               bool sf = false;
               if (!whole) {
                 const int pos = j * kTreeBlk + ct;
@@ -603,15 +634,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
               const unsigned m = __reduce_max_sync(0xffffffffu, vscale <= 3.4e38f ? __float_as_uint(vscale) : 0u);
               sf = __any_sync(0xffffffffu, sf);
               if (lane == 0) {
-                sh.vmax[slot * 4 + cw] = __uint_as_float(m);
-                sh.snf[slot * 4 + cw] = sf;
+                sh.vmax[slot * 4 + (cw & 1)] = __uint_as_float(m);
+                sh.snf[slot * 4 + (cw & 1)] = sf;
               }
             }
           }
         }
         if (isv && tail) {
           nf = __any_sync(0xffffffffu, nf);
-          if (lane == 0) sh.vnf[kb * 4 + cw] = nf;
+          if (lane == 0) sh.vnf[kb * 4 + (ct >> 5)] = nf;
         }
         if (!isv && (DIRECT ? lane == 0 : ct == 0)) sh.pok[slot] = pok;
         tc::fence_async_shared();
@@ -619,10 +650,11 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         if (lane == 0) {
           mbar_arrive(isv ? &sh.v_full[kb] : &sh.k_full[kb]);
         }
-        if (++kb == nbuf) { kb = 0; ++kround; }
-        slot = (slot + 1) % kNQ;
-        if (++raw == Y::RSD) { raw = 0; ++rround; }
+        if constexpr (DIRECT) {
+          if (++kb == NBK) { kb = 0; ++kpar; }
+        }
       }
+      J = end;
     }
     if (!run && lane == 0) fail(p, sh.abort);
   } else if (warp == kScoreWarp) {
@@ -633,7 +665,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     const uint64_t dk = first_kmajor(tiles + Y::K_OFF);
     bool ok = true;
     int unit = 0, kb = 0, kround = 0, sb = 0, sround = 0;
-    while (ok && walk.next(p, sg)) {
+    while (ok && next_segment()) {
       ok = __all_sync(0xffffffffu, wait(sh.q_ready, unit & 1, sh.abort));
       for (int j = sg.j0; j < sg.j1 && ok; ++j, ++J) {
         // the score buffer: P V of block J - 3 has read it
@@ -667,7 +699,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     const uint64_t dv = first_mnmajor(smem_u32(smem) + Y::V_OFF);
     bool ok = true;
     int vb = 0, vround = 0, sb = 0, sround = 0;
-    while (ok && walk.next(p, sg)) {
+    while (ok && next_segment()) {
       for (int j = sg.j0; j < sg.j1 && ok; ++j, ++J) {
         const int st = J & 1;
         bool fine = wait(&sh.v_full[vb], vround & 1, sh.abort);
@@ -710,7 +742,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       ++syncs;
       return __all_sync(0xffffffffu, fine);
     };
-    while (ok && walk.next(p, sg)) {
+    while (ok && next_segment()) {
       const int R = sg.L * p.g - sg.tile * kTreeRows;         // rows of the tile that exist
       const int x = sg.tile * kTreeRows + r;
       const bool row_ok = r < R, warp_ok = 32 * quarter < R;
@@ -730,14 +762,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
           if (!p.act_fp16) {
             // bf16 activations in fp16 tiles: the tile's largest |q| sets a power of two that
             // keeps every value in range (exact: bf16 has fewer bits than fp16)
-            float amax = 0.f;
+            __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float v[8];
-              unpack8<__nv_bfloat16>(u[i], v);
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-              for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
-            }
+              for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(reinterpret_cast<const __nv_bfloat162*>(&u[i])[e]));
+            float amax = fmaxf(__low2float(top), __high2float(top));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             if (lane == 0) sh.amax[warp] = amax;
@@ -747,9 +777,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
 #pragma unroll
             for (int i = 0; i < kSoftWarps; ++i) amax = fmaxf(amax, sh.amax[i]);
             int eq = 0;
-            if (amax > 0.f && amax <= 3.4e38f) eq = ilogbf(amax) - 13;
-            const float down = ldexpf(1.f, -eq);
-            qsc = ldexpf(qsc, eq);
+            // (values below 2^-87 of no weight in any score may become 0)
+            if (amax > 0.f && amax <= 3.4e38f) eq = max(exponent_of(amax) - 13, -100);
+            const float down = pow2i(-eq);
+            qsc *= pow2i(eq);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float v[8];
@@ -1075,26 +1106,20 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p) {
   griddep_wait();
   const TreeSeq s = tree_seq(p, b);
   if (i >= s.L * p.Hq) return;
-  long long W = 0, before = 0;
+  unsigned W = 0, before = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int bb = b0 + lane;
-    long long w = bb < p.B ? tree_work(p, tree_seq(p, bb)) : 0, q = bb < b ? w : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      w += __shfl_xor_sync(0xffffffffu, w, o);
-      q += __shfl_xor_sync(0xffffffffu, q, o);
-    }
-    W += w;
-    before += q;
+    const unsigned w = bb < p.B ? tree_work(p, tree_seq(p, bb)) : 0;
+    W += __reduce_add_sync(0xffffffffu, w);
+    before += __reduce_add_sync(0xffffffffu, bb < b ? w : 0);
   }
   const int tok = i / p.Hq, hq = i - tok * p.Hq, kvh = hq / p.g;
   const int x = tok * p.g + hq - kvh * p.g, tile = x / kTreeRows, r = x - tile * kTreeRows;
   const int nblk = tree_blocks(s.n);
-  const long long U0 = before + (static_cast<long long>(kvh) * tree_tile_rows(p, s.L) + tile / p.group) * nblk, U1 = U0 + nblk;
-  // group k covers [W k / K, W (k + 1) / K): the last that starts at or before U0, and the last
-  // that starts before U1
-  const int K = p.ctas / p.group;
-  const int c0 = static_cast<int>(((U0 + 1) * K + W - 1) / W) - 1, c1 = static_cast<int>((U1 * K + W - 1) / W) - 1;
+  const unsigned U0 = before + (kvh * tree_tile_rows(p, s.L) + tile / p.group) * (nblk + p.lead) + p.lead;
+  const TreeCut cut = tree_cut(p, W);
+  const int c0 = tree_share(cut, U0), c1 = tree_share(cut, U0 + nblk - 1);   // groups of its first and last block
   if (c0 == c1) return;
   // lane k describes the CTA of group c0 + k; the partial rows are then read eight at a time, so that their
   // loads overlap
@@ -1103,10 +1128,10 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p) {
   const float* o = p.ws_o + 4 * lane;
   for (int k0 = c0; k0 <= c1; k0 += 32) {
     const int c = k0 + lane;
-    long row = -1;
+    int row = -1;
     float mk = -INFINITY, lk = 0.f;
-    if (c <= c1 && tree_range(p, W, c) < tree_range(p, W, c + 1)) {
-      row = (2L * (c * p.group + tile % p.group) + (c == c0 ? 1 : 0)) * kTreeRows + r;
+    if (c <= c1) {
+      row = (2 * (c * p.group + tile % p.group) + (c == c0 ? 1 : 0)) * kTreeRows + r;
       const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * row);
       lk = v.y;
       if (lk != 0.f) mk = v.x;
@@ -1132,9 +1157,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p) {
         const int k = todo ? __ffs(todo) - 1 : -1;
         todo &= todo - 1;
         wt[t] = __shfl_sync(0xffffffffu, w, k & 31);
-        const long at = __shfl_sync(0xffffffffu, row, k & 31);
+        const int at = __shfl_sync(0xffffffffu, row, k & 31);
         v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k >= 0) v[t] = *reinterpret_cast<const float4*>(o + at * kD);
+        if (k >= 0) v[t] = *reinterpret_cast<const float4*>(o + static_cast<long>(at) * kD);
         else wt[t] = 0.f;
       }
 #pragma unroll
