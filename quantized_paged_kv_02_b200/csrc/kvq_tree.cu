@@ -355,6 +355,8 @@ kvq_status kvq_tree_attention(const kvq_cache_desc* c, const void* q, int num_q_
   p.ctas = plan.ctas;
   p.group = plan.group;
   p.lead = plan.lead;
+  p.shares = plan.kernel == 1 ? plan.ctas / plan.group : 1;
+  p.share_unit = static_cast<unsigned>(std::min((1LL << 32) / p.shares, 0xFFFFFFFFLL));
   p.fault = c->fault;
   const cudaError_t e = plan.kernel == 1 ? launch_tree_tc(p, g, stream) : launch_tree_simt(p, g.act_dtype, stream);
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

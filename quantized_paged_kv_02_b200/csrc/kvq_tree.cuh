@@ -38,6 +38,8 @@ struct TreeParams {
   void* out;
   int out_dtype;
   int splits, chunk, ctas, group, lead;
+  int shares;                // ctas / group
+  unsigned share_unit;       // 2^32 / shares, rounded down
   float* ws_o;
   float* ws_ml;
   int32_t* fault;
@@ -108,25 +110,21 @@ __device__ __forceinline__ int tree_blocks(int n) { return (n + kTreeBlk - 1) / 
 __device__ __forceinline__ unsigned tree_work(const TreeParams& p, const TreeSeq& s) {
   return s.L > 0 ? static_cast<unsigned>(tree_tile_rows(p, s.L) * p.H) * (tree_blocks(s.n) + p.lead) : 0;
 }
-// The cut of W into ctas / group shares: the first `more` of them have `each` + 1, the others `each`.
-// (32 bits: the entry point refuses calls that could pass 2^31; 64-bit divisions are a kilobyte of code
-// apiece, which a small call waits for.)
-struct TreeCut {
-  unsigned each, more;
-};
-__device__ __forceinline__ TreeCut tree_cut(const TreeParams& p, unsigned W) {
-  const unsigned K = p.ctas / p.group;
-  TreeCut c;
-  c.each = W / K;
-  c.more = W - c.each * K;
-  return c;
+// Start of share k when the work W is cut into p.shares about equal ones, or into shares of one block
+// where there are not as many (none but the last ones is empty): W k / shares, by a product
+// with 2^32 / shares (32 bits: the entry point refuses calls that could pass 2^31.  Divisions, and those
+// of 64 bits above all, were microseconds of a small call.)
+__device__ __forceinline__ unsigned tree_start(const TreeParams& p, unsigned W, int k) {
+  const unsigned few = min(static_cast<unsigned>(k), W);
+  return W <= static_cast<unsigned>(p.shares) ? few : k >= p.shares ? W : __umulhi(W, k * p.share_unit);
 }
-// Start of share k.
-__device__ __forceinline__ unsigned tree_start(const TreeCut& c, unsigned k) { return c.each * k + min(k, c.more); }
-// The share that holds position u.
-__device__ __forceinline__ int tree_share(const TreeCut& c, unsigned u) {
-  const unsigned head = c.more * (c.each + 1);
-  return static_cast<int>(u < head ? u / (c.each + 1) : c.more + (u - head) / max(c.each, 1u));
+// The share that holds position u < W: an estimate, and the steps that it is off.
+__device__ __forceinline__ int tree_share(const TreeParams& p, unsigned W, unsigned u) {
+  if (W <= static_cast<unsigned>(p.shares)) return static_cast<int>(u);
+  int k = min(p.shares - 1, static_cast<int>(__fdividef(static_cast<float>(u) * p.shares, static_cast<float>(W))));
+  while (tree_start(p, W, k) > u) --k;
+  while (tree_start(p, W, k + 1) <= u) ++k;
+  return k;
 }
 
 bool tree_tc_supported(const Geometry& g, int group);

@@ -33,6 +33,7 @@
 // power of two per tile).  P is one fp16 (11 bits) when the output is bf16 (8 bits) and the
 // tiles are fp16, which leaves the output's own rounding ten times larger than P's; otherwise
 // P is a hi + lo pair of 16-bit halves (two MMAs).  Scores, sums and O are binary32.
+#include <algorithm>
 #include <climits>
 #include <mutex>
 
@@ -381,16 +382,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     fence_mbar_init();
   }
   if (warp == kOutWarp) tc::tmem_alloc(sh.tmem, kTmemCols);
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();                                // (after the wait: the merge reads this call's inputs early)
   if (warp == 0) {
     // this CTA's share of the blocks, and the unit it begins in
     unsigned W = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32)
       W += __reduce_add_sync(0xffffffffu, b0 + lane < p.B ? tree_work(p, tree_seq(p, b0 + lane, blockIdx.x == 0)) : 0);
-    const TreeCut cut = tree_cut(p, W);
-    const unsigned w0 = tree_start(cut, blockIdx.x / p.group), w1 = tree_start(cut, blockIdx.x / p.group + 1);
+    const unsigned w0 = tree_start(p, W, blockIdx.x / p.group), w1 = tree_start(p, W, blockIdx.x / p.group + 1);
     unsigned before = 0;
     int at_b = 0, at_u = 0, at_pos = 0;
 #pragma unroll 1
@@ -1096,16 +1096,17 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
   }
 }
 
-// Joins the partial results of units cut between CTAs: one warp per query row, 4 channels
-// per lane.  A unit that lies in one CTA's range was written by that CTA.
-__global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p) {
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);          // (token, head) of the sequence
-  // the schedule depends on the call's inputs only, which this call does not write; they are
-  // read after the wait all the same, since an earlier kernel of the stream may have
-  griddep_wait();
+// Joins the partial results of units cut between CTAs: a warp per query row, 4 channels per lane, and
+// `per_warp` rows one after another, so that large calls read the schedule once for many rows.  A
+// unit that lies in one CTA's range was written by that CTA.  What bounds it is the chain of loads: the
+// schedule is worked out before the wait for the attention kernel (which let this one start only after
+// its own wait: what ran before it is complete), and N partial rows are on their way at a time: 16 where
+// one row is all a warp has (1032 tokens, 17 parts a row: the call takes 20.5 us, 25 with 8 behind a look
+// at their sums), 8 where more warps per SM hide the loads.
+template <int N>
+__global__ void __launch_bounds__(256, N == 16 ? 2 : 4) tree_merge_kernel(TreeParams p, int per_warp) {
+  const int b = blockIdx.z, kvh = blockIdx.y, lane = threadIdx.x & 31;
   const TreeSeq s = tree_seq(p, b);
-  if (i >= s.L * p.Hq) return;
   unsigned W = 0, before = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -1114,74 +1115,76 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeParams p) {
     W += __reduce_add_sync(0xffffffffu, w);
     before += __reduce_add_sync(0xffffffffu, bb < b ? w : 0);
   }
-  const int tok = i / p.Hq, hq = i - tok * p.Hq, kvh = hq / p.g;
-  const int x = tok * p.g + hq - kvh * p.g, tile = x / kTreeRows, r = x - tile * kTreeRows;
   const int nblk = tree_blocks(s.n);
-  const unsigned U0 = before + (kvh * tree_tile_rows(p, s.L) + tile / p.group) * (nblk + p.lead) + p.lead;
-  const TreeCut cut = tree_cut(p, W);
-  const int c0 = tree_share(cut, U0), c1 = tree_share(cut, U0 + nblk - 1);   // groups of its first and last block
-  if (c0 == c1) return;
-  // lane k describes the CTA of group c0 + k; the partial rows are then read eight at a time, so that their
-  // loads overlap
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* o = p.ws_o + 4 * lane;
-  for (int k0 = c0; k0 <= c1; k0 += 32) {
-    const int c = k0 + lane;
-    int row = -1;
-    float mk = -INFINITY, lk = 0.f;
-    if (c <= c1) {
-      row = (2 * (c * p.group + tile % p.group) + (c == c0 ? 1 : 0)) * kTreeRows + r;
-      const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * row);
-      lk = v.y;
-      if (lk != 0.f) mk = v.x;
-      else row = -1;                                          // nothing seen
+  const unsigned unit0 = before + p.lead;                     // the sequence's first unit's first block
+  int last = -1, member = 0, c0 = 0, c1 = 0;                  // the tile before; the shares of its first and last block
+  bool waited = false;
+#pragma unroll 1
+  for (int k = 0; k < per_warp; ++k) {
+    const int x = (blockIdx.x * per_warp + k) * 8 + (threadIdx.x >> 5);   // row of the sequence and kv head
+    const int tile = x / kTreeRows, r = x % kTreeRows;
+    if (x < s.L * p.g && tile != last) {
+      last = tile;
+      const int group = tile / p.group;
+      member = tile - group * p.group;
+      const unsigned U0 = unit0 + (kvh * tree_tile_rows(p, s.L) + group) * (nblk + p.lead);
+      c0 = tree_share(p, W, U0);
+      c1 = tree_share(p, W, U0 + nblk - 1);
     }
-    float mx = mk;
+    if (!waited) griddep_wait();
+    waited = true;
+    if (x >= s.L * p.g) return;
+    if (c0 == c1) continue;
+    auto row_of = [&](int c) { return (2 * (c * p.group + member) + (c == c0 ? 1 : 0)) * kTreeRows + r; };
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* o = p.ws_o + 4 * lane;
+#pragma unroll 1
+    for (int k0 = c0; k0 <= c1; k0 += N) {
+      // lane t < N has the (offset, sum) of group k0 + t
+      const int n = min(N, c1 - k0 + 1);
+      float2 ml = make_float2(0.f, 0.f);
+      if (lane < n) ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * row_of(k0 + lane));
+      float4 v[N];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    if (mx > M) {
-      const float f = M == -INFINITY ? 0.f : ex2(M - mx);
-      M = mx;
-      L *= f;
-      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-    }
-    const float w = row >= 0 ? ex2(mk - M) : 0.f;
-    L = row >= 0 ? fmaf(lk, w, L) : L;
-    unsigned todo = __ballot_sync(0xffffffffu, row >= 0);
-    while (todo) {
-      float4 v[8];
-      float wt[8];
+      for (int t = 0; t < N; ++t)
+        v[t] = t < n ? *reinterpret_cast<const float4*>(o + static_cast<long>(row_of(k0 + t)) * kD) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float mx = ml.y != 0.f ? ml.x : -INFINITY;              // (a sum of 0: nothing seen, and v is zeros)
+      const float mk = mx;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const int k = todo ? __ffs(todo) - 1 : -1;
-        todo &= todo - 1;
-        wt[t] = __shfl_sync(0xffffffffu, w, k & 31);
-        const int at = __shfl_sync(0xffffffffu, row, k & 31);
-        v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k >= 0) v[t] = *reinterpret_cast<const float4*>(o + static_cast<long>(at) * kD);
-        else wt[t] = 0.f;
+      for (int d = N / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      mx = __shfl_sync(0xffffffffu, mx, 0);
+      if (mx > M) {
+        const float f = M == -INFINITY ? 0.f : ex2(M - mx);
+        M = mx;
+        L *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
       }
+      const float w = ml.y != 0.f ? ex2(mk - M) : 0.f;
+      if (ml.y != 0.f) L = fmaf(ml.y, w, L);
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        acc.x = fmaf(v[t].x, wt[t], acc.x);
-        acc.y = fmaf(v[t].y, wt[t], acc.y);
-        acc.z = fmaf(v[t].z, wt[t], acc.z);
-        acc.w = fmaf(v[t].w, wt[t], acc.w);
+      for (int t = 0; t < N; ++t) {
+        const float wt = __shfl_sync(0xffffffffu, w, t);
+        acc.x = fmaf(v[t].x, wt, acc.x);
+        acc.y = fmaf(v[t].y, wt, acc.y);
+        acc.z = fmaf(v[t].z, wt, acc.z);
+        acc.w = fmaf(v[t].w, wt, acc.w);
       }
     }
-  }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-  const float inv = L != 0.f ? 1.f / L : 0.f;
-  const long e0 = (static_cast<long>(s.q0) * p.Hq + i) * kD + 4 * lane;
-  if (p.out_dtype == KVQ_DTYPE_FP32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + e0) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  } else {
-    const bool bf = p.out_dtype == KVQ_DTYPE_BF16;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + e0) =
-        bf ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv))
-           : make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
+    for (int d = N / 2; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    L = __shfl_sync(0xffffffffu, L, 0);
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    const int tok = x / p.g;
+    const long e0 = ((static_cast<long>(s.q0) + tok) * p.Hq + static_cast<long>(kvh) * p.g + (x - tok * p.g)) * kD + 4 * lane;
+    if (p.out_dtype == KVQ_DTYPE_FP32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + e0) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+      const bool bf = p.out_dtype == KVQ_DTYPE_BF16;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + e0) =
+          bf ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv))
+             : make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
+    }
   }
 }
 
@@ -1200,7 +1203,13 @@ cudaError_t launch(const TreeParams& p, const Geometry& g, cudaStream_t s) {
   tree_tc_kernel<CD, PT, HILO><<<p.ctas, kThreads, Y::BYTES, s>>>(p, rows);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_dependent(tree_merge_kernel, dim3((p.max_tree * p.Hq + 7) / 8, p.B), dim3(256), 0, s, p);
+  // rows per warp: about four times the CTAs that the SMs hold (most find units that were not cut)
+  const long most = static_cast<long>(p.max_tree) * p.g, warps = most * p.H * p.B;
+  const bool one = warps <= 2L * 8 * p.ctas;
+  const int per_warp = one ? 1 : static_cast<int>(std::min((warps + 16L * 8 * p.ctas - 1) / (16L * 8 * p.ctas), (most + 7) / 8));
+  const dim3 grid(static_cast<unsigned>((most + 8L * per_warp - 1) / (8L * per_warp)), p.H, p.B);
+  return one ? launch_dependent(tree_merge_kernel<16>, grid, dim3(256), 0, s, p, per_warp)
+             : launch_dependent(tree_merge_kernel<8>, grid, dim3(256), 0, s, p, per_warp);
 }
 
 }  // namespace
