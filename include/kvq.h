@@ -559,8 +559,10 @@ kvq_status kvq_tree_workspace_size(const kvq_cache_desc* cache, int batch, int n
  *   itself the result is kvq_decode_attention's.
  *   Dense caches.  head_dim 128 with block_size 16 (not PER_CHANNEL) runs on the 5th-generation
  *   tensor cores, any GQA group; other geometries on a CUDA-core kernel.  With BF16 output and
- *   8-bit or FP16 caches the tensor-core kernel rounds the probabilities to fp16 (2^-12 relative,
- *   an eighth of the output's own half step); otherwise they keep 16 bits or more.
+ *   8-bit or FP16 caches the tensor-core kernel rounds the probabilities to fp16 (2^-11 relative
+ *   at most, an eighth of the output's own half step); otherwise they keep 16 bits or more.
+ *   There, batch x kv heads x blocks of 64 positions of max_context (x rows of four tiles of 128
+ *   query rows) has to stay below 2^27: KVQ_ERR_UNSUPPORTED.
  *   INT4 / INT2: KVQ_ERR_UNSUPPORTED (a rejected draft could not be taken back out of the ring).
  */
 kvq_status kvq_tree_attention(const kvq_cache_desc* cache, const void* q, int num_q_tokens,

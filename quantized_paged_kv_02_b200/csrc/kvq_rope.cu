@@ -18,6 +18,11 @@
 // contiguous, and the rotation may run in place.  The rows of a CTA's tokens form one list, 32 (64
 // for head_dim 64) at a time, the loads of the next two turns in flight.  The quantizers are kvq_write's, fed
 // with the rotated binary32 values (no rounding to 16 bits in between).
+//
+// Measured (B200): 16411 tokens of 32 / 8 bf16 heads, 64 of 128 dimensions interleaved, 61 us, 5.5 TB/s
+// (one token per CTA 76 us: every CTA waited for its own sines); 24 tokens 6 us, a launch and one chain of
+// loads; 32768 tokens of 64 / 8 heads with quantize-on-write to INT8 231 us, 5.5 TB/s of the bytes it
+// cannot do without.
 #include <algorithm>
 #include <climits>
 #include <cmath>

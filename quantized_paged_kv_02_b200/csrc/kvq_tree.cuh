@@ -10,7 +10,7 @@ constexpr int kTreeMax = 1024;       // drafted tokens per sequence at most
 constexpr int kTreeGroup = 4;        // CTAs that share a walk at most
 constexpr int kTreeRows = 128;       // tensor-core kernel: query rows per tile
 constexpr int kTreeBlk = 64;         // ... and cached tokens per block
-constexpr int kTreeLead = 6;         // a unit's start and end take as long as this many blocks
+constexpr int kTreeLead = 14;        // a unit's start and end take as long as this many blocks
 
 struct TreePlan {
   int kernel;          // 0 CUDA cores, 1 tensor cores (tcgen05)
@@ -91,9 +91,9 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t* row, int pos, int 
 }
 
 // Block-balanced schedule of the tensor-core kernel.  A unit is one (sequence, kv head, row of
-// `group` tiles of 128 query rows) and has ceil(n / 64) blocks; the blocks of all units, in the
-// order (sequence, kv head, row of tiles), are cut into ctas / group contiguous ranges, one per
-// group of CTAs.  The CTAs of a group walk the same blocks at the same time, each for its own tile
+// `group` tiles of 128 query rows) and has ceil(n / 64) blocks; the blocks of all units (and `lead`
+// before each unit's own, for what a unit costs besides), in the order (sequence, kv head, row of
+// tiles), are cut into ctas / group contiguous ranges, one per group of CTAs.  The CTAs of a group walk the same blocks at the same time, each for its own tile
 // of the row, so that the cache's bytes come from DRAM once for all of them (trees wider than one
 // tile; with tiles as units of their own the tiles of a sequence were read at different times, and
 // DRAM was the bound).  A CTA has at most two segments that do not hold a whole unit: one that

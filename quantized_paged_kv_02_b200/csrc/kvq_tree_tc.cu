@@ -2,24 +2,34 @@
 // accumulators in tensor memory): head_dim 128, block size 16, INT8 / FP8 / BF16 / FP16 caches.
 //
 // A unit is one tile of 128 query rows (row r: drafted token r / g, head r % g) of one
-// (sequence, kv head); it walks the sequence's positions in blocks of 128.  One persistent CTA
+// (sequence, kv head); it walks the sequence's positions in blocks of 64.  One persistent CTA
 // per SM takes an equal share of all units' blocks (kvq_tree.cuh), so that a few long
 // sequences and many short ones both fill the machine; a unit cut between CTAs leaves partial
 // results (unnormalised O, exponent offset, sum) that tree_merge_kernel joins.
 //
-// Inside a CTA the blocks go to two streams in turn, each with its own scores, running
-// maximum, sum and output accumulator in tensor memory (S0 S1 O0 O1: all 512 columns), joined
-// once per unit.  So the chain of one block (S = Q K^T, softmax, O += P V) never waits for the
-// softmax of the block before it, and while one stream's warps work on scores the tensor
-// cores work for the other: with few query rows the bound is the cache's bytes, and that
-// needs a block about every 1500 cycles, half of one chain's length.
+// Inside a CTA the blocks go to two streams in turn, each with its own running maximum, sum and
+// output accumulator, joined once per unit: the chain of one block (S = Q K^T, softmax, O += P V)
+// never waits for the softmax of the block before it.  Tensor memory holds three score buffers of 64
+// columns (one per stream in use, one ahead; P replaces the scores it came from), Q (64) and the two
+// accumulators (128 each): all 512 columns.
 //
 //   warps 0-3, 4-7  softmax of stream 0 / 1: one query row per thread;
-//   warp 8          producer: block-table entries, one bulk copy per page record into a ring of
-//                   half blocks (16-bit caches: four TMA tensor copies per page straight into
-//                   the K / V tiles);
-//   warp 9          MMA issuer;
-//   warps 10-13     K converters, 14-17 V converters: codes -> fp16 tiles (exact).
+//   warp 8          producer: block-table entries (32 pages at a time, the next 32 sent for into L2),
+//                   one bulk copy per page record into a ring of six blocks (16-bit caches: four
+//                   warps, each with one of a page's four TMA tensor copies straight into the tiles);
+//   warp 9          issues S = Q K^T;  warp 18 issues O += P V;
+//   warps 10-13     K converters, 14-17 V converters: codes -> fp16 tiles (exact), two warps per block.
+//
+// Measured (B200; GB/s of cache read, bf16 results): trees of 16, 64 / 8 heads over 24 x 16384 INT8
+// 309 us, 2.7 TB/s; ragged trees, 32 / 8 heads over 64 x 1024..8192 FP8 233 us, 2.7 TB/s; trees of 64
+// over 8 x 16384 bf16 397 us, 1.4 TB/s and 690 TFLOP/s (hi + lo P: three products for two).  Bytes are
+// not the bound, nor the tensor pipe (a third busy): it is instruction issue.  About 7000 warp
+// instructions go into 128 positions (a softmax warp 450 per 64, a converter warp 300 per 64), 57% of
+// the issue slots, and the rest are waits on latencies that 19 warps do not cover.  What follows:
+// scores, weights and sums are packed pairs, blocks that every row sees skip the maximum, two converter
+// warps per block rather than four (331 -> 317 us), and the roles' loops are kept small, since together
+// they have to fit the instruction cache (5% of the time when they did not).  Starting and ending a
+// unit costs 8 us of a CTA, which the shares count.
 //
 // Query i sees the prefix and the drafted tokens of its mask row.  Blocks that hold prefix
 // only, on pages that passed their table check, take a path without per-score tests; in the
@@ -867,7 +877,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
           // columns before column c0) into the new domain
           auto rebase = [&](bool ask, float mx, int c0) {
             float f = 1.f;
-            if (ask) {
+            if (ask && mx > -INFINITY) {
               const float mn = ceilf(mx);
               f = m == -INFINITY ? 0.f : pow2i(static_cast<int>(fmaxf(m - mn, -1000.f)));
               m = moff = mn;

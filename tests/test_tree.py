@@ -147,6 +147,7 @@ def test_tree_refusals():
                 dict(d=_desc(pages=0))):
         assert call(**bad) == 1, bad
     assert call(mt=1025, mw=33) == 2
+    assert call(mc=1 << 30, B=8) == 2                            # more blocks than the schedule can count
     assert call(d=_desc(cache_dtype=6, scale_mode=4, block_size=64)) == 2
     # the CUDA-core kernel's partials are per query row: more rows than batch * max_tree do not fit
     d = _desc(head_dim=64)
@@ -253,6 +254,23 @@ def test_one_position_far_above_the_rest(cd, mode, act, up):
     want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
     for od in (F32, B16):
         check(run(gc, w, q, starts, mask, most, od), want, spread, od)
+
+
+@gpu
+def test_scores_of_minus_infinity_and_vanishing_queries():
+    """A prefix whose scores overflow to -inf weighs nothing; q next to 0 weighs every position alike."""
+    w, q, starts, sees, mask, most = make("bf16", "none", "bf16", 4, 1, 128, 16, [300, 90], [3, 90], seed=6)
+    q = q.abs() + 4
+    w.k[:150] = -1e38                                           # (all of the first blocks, of both streams)
+    oc, gc = helpers.oracle_cache(w), helpers.gpu_cache(w)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+
+    check(run(gc, w, q, starts, mask, most), want, spread, F32)
+    w, q, starts, sees, mask, most = make("int8", "per_token_head", "bf16", 4, 1, 128, 16, [300], [3], seed=6)
+    q = (q.float() * 1e-37).to(torch.bfloat16)
+    oc, gc = helpers.oracle_cache(w), helpers.gpu_cache(w)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    check(run(gc, w, q, starts, mask, most), want, spread, F32)
 
 
 @gpu
