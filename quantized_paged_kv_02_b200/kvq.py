@@ -296,6 +296,24 @@ def _at(t, dev, what):
     return t.data_ptr()
 
 
+def _like(x, stream, shape=None, dtype=None):
+    """A dense tensor like x, allocated for the stream that writes it: memory of the current stream could
+    still be in use there, and a released workspace of it would be handed out again too early."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _like(x, None, shape, dtype)
+    if shape is None:
+        return torch.empty_like(x) if dtype is None else torch.empty_like(x, dtype=dtype)
+    return x.new_empty(shape, dtype=dtype)
+
+
+def _freqs(t, rope, dev):
+    """Address of a rope's frequencies."""
+    if t.dtype != torch.float64 or not t.is_contiguous() or 2 * t.numel() < rope.rot_dim:
+        raise ValueError("freqs must be contiguous float64 and have rot_dim / 2 entries")
+    return _at(t, dev, "freqs")
+
+
 def _rows(t, what):
     """(tokens, heads, dim, token stride) of a [T][heads][dim] tensor whose rows are dense (a view into
     fused projection rows is fine)."""
@@ -334,6 +352,8 @@ def kvq_rope_frequencies(rope):
 def kvq_rope(rope, freqs, positions, q=None, k=None, q_out=None, k_out=None, stream=None):
     """Rotate q [T, Hq, D] and / or k [T, H, D] (token strides as they are) into q_out / k_out
     (given, or allocated dense); an output may be its input."""
+    if q is None and k is None:
+        raise ValueError("neither q nor k to rotate")
     act = q.dtype if q is not None else k.dtype
     if act not in _ACT_CODE:
         raise TypeError("activations must be bfloat16 or float16, got %s" % act)
@@ -350,7 +370,7 @@ def kvq_rope(rope, freqs, positions, q=None, k=None, q_out=None, k_out=None, str
         if Tx != T or Dx != D:
             raise ValueError("q and k must have the same tokens and head_dim")
         if out is None:
-            out = torch.empty_like(x)                  # dense
+            out = torch.empty_like(x) if stream is None else _like(x, stream)
             os = H * D
         else:
             shape = _rows(out, what + "_out")
@@ -360,11 +380,11 @@ def kvq_rope(rope, freqs, positions, q=None, k=None, q_out=None, k_out=None, str
         if x.dtype != act or out.dtype != act:
             raise TypeError("q, k and their outputs must have one type")
         args += (_at(x, dev, what), xs, H, _at(out, dev, what), os)
-        if x is q:
+        if what == "q":
             q_out = out
         else:
             k_out = out
-    st = lib.kvq_rope(ctypes.byref(rope), _at(freqs, dev, "freqs"), _ACT_CODE[act], D, _index(positions, T, dev, "positions"), T,
+    st = lib.kvq_rope(ctypes.byref(rope), _freqs(freqs, rope, dev), _ACT_CODE[act], D, _index(positions, T, dev, "positions"), T,
                       *args, _raw_stream(stream, dev))
     if st:
         _check(st, "kvq_rope")
@@ -388,7 +408,7 @@ def kvq_rope_write(desc, rope, freqs, positions, q, k_new, v_new, slot_mapping, 
         if Tq != T or Dq != D:
             raise ValueError("q must have the tokens and head_dim of k_new")
         if q_out is None:
-            q_out = torch.empty_like(q)                # dense
+            q_out = torch.empty_like(q) if stream is None else _like(q, stream)
             qos = hq * D
         else:
             To, ho, Do, qos = _rows(q_out, "q_out")
@@ -397,7 +417,7 @@ def kvq_rope_write(desc, rope, freqs, positions, q, k_new, v_new, slot_mapping, 
         if q.dtype != act or q_out.dtype != act:
             raise TypeError("q and q_out must have the cache's activation type")
         qp, qop = _at(q, dev, "q"), _at(q_out, dev, "q_out")
-    st = lib.kvq_rope_write(ctypes.byref(desc), ctypes.byref(rope), _at(freqs, dev, "freqs"),
+    st = lib.kvq_rope_write(ctypes.byref(desc), ctypes.byref(rope), _freqs(freqs, rope, dev),
                             _index(positions, T, dev, "positions"), T, qp, qs, hq, qop, qos, _at(k_new, dev, "k_new"), ks,
                             _at(v_new, dev, "v_new"), vs, _index(slot_mapping, T, dev, "slot_mapping"),
                             _raw_stream(stream, dev))
@@ -587,17 +607,19 @@ class PagedKVCache:
 
     def rope_write(self, rope, positions, q, k_new, v_new, slot_mapping, q_out=None, stream=None):
         """Rotate q and k_new, store the rotated keys and v_new; returns the rotated q."""
+        _at(self.pages, _here(), "the cache")
         return kvq_rope_write(self.desc, rope.desc, rope.freqs, positions, q, k_new, v_new, slot_mapping, q_out,
                               stream)
 
     def gather(self, slots, k_out=None, v_out=None, stream=None):
         """(K, V) rows of the listed slots, [rows, H, D] of the activation type."""
+        _at(self.pages, _here(), "the cache")
+        shape = (slots.numel(), self.num_kv_heads, self.head_dim)
+        dt = torch.bfloat16 if self.act_dtype == "bf16" else torch.float16
         if k_out is None:
-            shape = (slots.numel(), self.num_kv_heads, self.head_dim)
-            dt = torch.bfloat16 if self.act_dtype == "bf16" else torch.float16
-            k_out = torch.empty(shape, dtype=dt, device=self.device)
+            k_out = _like(self.pages, stream, shape, dt)
         if v_out is None:
-            v_out = torch.empty_like(k_out)
+            v_out = _like(self.pages, stream, shape, dt)
         return kvq_gather(self.desc, slots, k_out, v_out, stream)
 
     def tree_workspace_size(self, batch, num_q_heads, max_tree, max_context):
@@ -605,18 +627,20 @@ class PagedKVCache:
 
     def tree_attention(self, q, q_start, max_tree, tree_mask, block_tables, context_lens, max_context, out=None,
                        out_dtype=torch.float32, workspace=None, softmax_scale=0.0, stream=None):
+        _at(self.pages, _here(), "the cache")
         if out is None:
-            out = torch.empty_like(q, dtype=out_dtype)
+            out = _like(q, stream, None, out_dtype)
         if workspace is None:
             n = self.tree_workspace_size(context_lens.numel(), q.shape[1], max_tree, max_context)
-            workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device) if n else None
+            workspace = _like(q, stream, (n,), torch.uint8) if n else None
         return kvq_tree_attention(self.desc, q, q_start, max_tree, tree_mask, block_tables, context_lens,
                                   max_context, out, workspace, softmax_scale, stream)
 
     def tree_commit(self, path, accepted, q_start, block_tables, context_lens, new_lens=None, stream=None):
         """Keep each sequence's accepted path; returns the new context lengths."""
+        _at(self.pages, _here(), "the cache")
         if new_lens is None:
-            new_lens = torch.empty_like(context_lens)
+            new_lens = _like(context_lens, stream)
         return kvq_tree_commit(self.desc, path, accepted, q_start, block_tables, context_lens, new_lens, stream)
 
     def flush_ring(self, seq_ids, positions, block_ids, stream=None):

@@ -240,9 +240,14 @@ def test_rope_wrapper_checks():
         r.apply(pos, q, q_out=q[:, :1])
     with pytest.raises(TypeError):
         r.apply(pos, q.float())
-    for bad in ((pos.cpu(), q), (pos, q.cpu())):                    # host tensors
+    for bad in ((pos.cpu(), q), (pos, q.cpu()), (pos,)):            # host tensors, nothing to rotate
         with pytest.raises(ValueError):
             r.apply(*bad)
+    for freqs in (r.freqs[:-1], r.freqs.float()):
+        with pytest.raises(ValueError):
+            kvq.kvq_rope(r.desc, freqs, pos, q)
+    a, b = r.apply(pos, q, q)                                       # one tensor as both
+    assert torch.equal(a, b) and torch.equal(a, r.apply(pos, q)[0])
 
 
 def _cache(cd, act, mode, nb, bs, H, D, seed=0):

@@ -430,6 +430,27 @@ def test_two_streams_graph_and_backgrounds():
 
 
 @gpu
+def test_workspace_of_a_call_on_another_stream_is_not_handed_out():
+    """The call's own workspace and output belong to its stream: what the current stream allocates and
+    fills meanwhile is other memory."""
+    w, q, starts, sees, mask, most = make("fp8", "per_head", "bf16", 8, 2, 128, 16, [3000, 2500], [16, 9])
+    gc = helpers.gpu_cache(w, static=helpers.oracle_static_scales(w))
+    args = (q.cuda(), starts.cuda(), most, mask.cuda(), w.block_tables.cuda(), w.context_lens.cuda(), w.max_context)
+    want = gc.tree_attention(*args)
+    n = gc.tree_workspace_size(2, 8, most, w.max_context)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100000)
+        got = gc.tree_attention(*args, stream=s)
+        for _ in range(20):
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+@gpu
 def test_draft_verify_and_commit():
     """A run of the operators as a serving step uses them: the drafted rows rotated by their depth and
     written, the tree attended, its accepted path committed, and the next decode step equal to
@@ -480,6 +501,9 @@ def test_wrapper_checks():
     for bad in (dict(tree_mask=a["tree_mask"].long()), dict(q_start=a["q_start"].long())):
         with pytest.raises(TypeError):
             gc.tree_attention(**{**a, **bad})
+    cold = kvq.PagedKVCache("int8", "bf16", "per_token_head", gc.num_blocks, 16, 2, 128, device="cpu")
+    with pytest.raises(ValueError):
+        cold.tree_attention(**a)
     # a host tensor is refused, not dereferenced
     for name in ("q", "q_start", "tree_mask", "block_tables", "context_lens"):
         with pytest.raises(ValueError):
