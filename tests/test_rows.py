@@ -170,3 +170,55 @@ def test_commit_leaves_bad_paths_alone():
     none = torch.zeros((8, 0), dtype=torch.int32, device="cuda")
     got = gc.tree_commit(none, torch.zeros(8, dtype=torch.int32, device="cuda"), starts.cuda(), w.block_tables.cuda(), w.context_lens.cuda())
     assert got.tolist() == [50] * 8 and torch.equal(gc.records().cpu(), want)
+
+
+@pytest.mark.gpu
+def test_gather_and_commit_replay_in_a_graph_and_on_a_stream():
+    """Captured once, replayed on other slots, paths and lengths; and the same calls on a stream of their own."""
+    H, D, bs, B, L = 2, 128, 16, 3, 9
+    g = torch.Generator().manual_seed(8)
+    table = torch.randperm(24, generator=g)[:18].view(B, 6).int().cuda()
+    rows = torch.randn((2, B * 90, H, D), generator=g).to(torch.bfloat16).cuda()
+    every = (table.long()[:, torch.arange(90, device="cuda") // bs] * bs + torch.arange(90, device="cuda") % bs).int().reshape(-1)
+    starts = torch.arange(B + 1, dtype=torch.int32, device="cuda") * L
+
+    def fresh():
+        c = kvq.PagedKVCache("int8", "bf16", "per_token_head", 24, bs, H, D)
+        c.write(rows[0], rows[1], every)
+        return c
+
+    def draw(seed):
+        r = torch.Generator().manual_seed(seed)
+        acc = torch.randint(0, 6, (B,), generator=r)
+        path = torch.stack([torch.randperm(L, generator=r)[:5].sort().values for _ in range(B)])
+        lens = torch.randint(L, 90, (B,), generator=r)
+        slots = every.cpu()[torch.randint(0, every.numel(), (40,), generator=r)]
+        return [x.int().cuda() for x in (acc, path, lens, slots)]
+
+    def direct(args, stream=None):
+        c = fresh()
+        acc, path, lens, slots = args
+        torch.cuda.synchronize()
+        new = c.tree_commit(path, acc, starts, table, lens, stream=stream)
+        k, v = c.gather(slots, stream=stream)
+        torch.cuda.synchronize()
+        return new, k, v, c.pages.clone()
+
+    c = fresh()
+    acc, path, lens, slots = draw(0)
+    new, k, v = torch.empty_like(lens), *(torch.empty((40, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.tree_commit(path, acc, starts, table, lens, new)
+        c.gather(slots, k, v)
+    for seed in (1, 2, 3):
+        args = draw(seed)
+        for at, x in zip((acc, path, lens, slots), args):
+            at.copy_(x)
+        c.pages.copy_(fresh().pages)
+        graph.replay()
+        torch.cuda.synchronize()
+        for want in (direct(args), direct(args, torch.cuda.Stream())):
+            assert all(torch.equal(a, b) for a, b in zip((new, k, v, c.pages), want))
+    assert c.read_fault() == (0, 0)
