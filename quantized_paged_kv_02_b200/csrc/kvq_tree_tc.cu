@@ -23,8 +23,8 @@
 // Measured (B200; GB/s of cache read, bf16 results): trees of 16, 64 / 8 heads over 24 x 16384 INT8
 // 309 us, 2.7 TB/s; ragged trees, 32 / 8 heads over 64 x 1024..8192 FP8 233 us, 2.7 TB/s; trees of 64
 // over 8 x 16384 bf16 397 us, 1.4 TB/s and 690 TFLOP/s (hi + lo P: three products for two).  Bytes are
-// not the bound, nor the tensor pipe (a third busy): it is instruction issue.  About 7000 warp
-// instructions go into 128 positions (a softmax warp 450 per 64, a converter warp 300 per 64), 57% of
+// not the bound, nor the tensor pipe (31% busy; 47% for bf16): it is instruction issue.  About 6800 warp
+// instructions go into 128 positions (a softmax warp 450 per 64, a converter warp 300 per 64), 52% of
 // the issue slots, and the rest are waits on latencies that 19 warps do not cover.  What follows:
 // scores, weights and sums are packed pairs, blocks that every row sees skip the maximum, two converter
 // warps per block rather than four (331 -> 317 us), and the roles' loops are kept small, since together
