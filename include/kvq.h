@@ -554,9 +554,11 @@ kvq_status kvq_tree_workspace_size(const kvq_cache_desc* cache, int batch, int n
  *                 [0, num_q_tokens].
  *   workspace     as kvq_decode_attention: kvq_tree_workspace_size() bytes, no initialisation,
  *                 not shared by calls that overlap on the GPU.
- *   Positions on a block id out of range are left out (counted, KVQ_FAULT_BLOCK).  Infinities and
- *   NaN in drafted rows reach only the queries that see them.  With one drafted token that sees
- *   itself the result is kvq_decode_attention's.
+ *   Positions on a block id out of range are left out (counted, KVQ_FAULT_BLOCK).  What a drafted row
+ *   holds (values of any size, infinities, NaN, the bytes of a slot that was never written) reaches only
+ *   the queries that see it.  With one drafted token that sees itself the result is
+ *   kvq_decode_attention's.  With per-token scales the V scales that a query sees may lie anywhere from
+ *   2^-84 to 2^84 (rows with smaller ones lose bits).
  *   Dense caches.  head_dim 128 with block_size 16 (not PER_CHANNEL) runs on the 5th-generation
  *   tensor cores, any GQA group; other geometries on a CUDA-core kernel.  With BF16 output and
  *   8-bit or FP16 caches the tensor-core kernel rounds the probabilities to fp16 (2^-11 relative

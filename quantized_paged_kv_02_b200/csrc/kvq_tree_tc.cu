@@ -65,7 +65,8 @@ constexpr int kNS = 3;               // score buffers: one in use per stream, on
 // hence after the softmax of all blocks up to that: the slot of block J - 8 is free
 constexpr int kNQ = 8;
 constexpr float kRebase = 8.f;       // log2 headroom before the running maximum is re-based,
-constexpr float kMostSum = 8192.f;   // or the sum of 32 weights that asks for it
+constexpr float kMostSum = 8192.f;   // or the sum of 32 weights, times the block's largest V scale, that asks for it
+constexpr float kMostE = 90.f;       // log2 of the weights themselves stays below about this (V scales below 1)
 // TMEM columns: scores / P of block J in [64 (J % 3), +64), Q in [192, 256), O of stream s in
 // [256 + 128 s, +128)
 constexpr uint32_t kTmemCols = 512, kTmQ = 192, kTmO = 256;
@@ -87,7 +88,8 @@ struct Layout {
   static constexpr int RAW_OFF = V_OFF + NBV * kTile;
   static constexpr int KS_OFF = RAW_OFF + RS * kPPB * REC;      // float [kNQ][64] K scales (PT)
   static constexpr int VS_OFF = KS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [kNQ][64]: V scales
-  static constexpr int KQ_OFF = VS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [8][64]: a softmax warp's score factors (PT)
+  static constexpr int VL_OFF = VS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [kNQ][64]: log2 of V scales
+  static constexpr int KQ_OFF = VL_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [8][64]: a softmax warp's score factors (PT)
   static constexpr int EX_OFF = KQ_OFF + (PT ? kSoftWarps * kTreeBlk * 4 : 0);   // float [2][2][128], int [4]: a unit's end
   static constexpr int WALK_OFF = EX_OFF + 4 * kTreeRows * 4 + 16;        // Walk [warps]
   static constexpr int MISC_OFF = WALK_OFF + (kThreads / 32 + 1) / 2 * 128;
@@ -159,7 +161,7 @@ struct Shared {
   uint64_t *raw_full, *raw_empty, *tile_full, *k_full, *k_free, *v_full, *v_free, *s_full, *s_free, *p_full, *pv_done,
       *q_ready, *o_full, *sync, *fin;
   int *pages, *pok, *snf, *vnf, *sched;
-  float *vmax, *amax, *ks, *vs;
+  float *vmax, *amax, *ks, *vs, *vl;
   uint32_t* tmem;
   volatile int* abort;
 };
@@ -248,6 +250,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// x 2^d for an integer d <= 0, in two steps (x may be as large as 2^d is small).
+__device__ __forceinline__ float times_2(float x, float d) {
+  const float h = truncf(0.5f * d);
+  return x * ex2(h) * ex2(d - h);
 }
 
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
@@ -344,6 +352,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     sh.abort = reinterpret_cast<volatile int*>(sh.sched + 7);
     sh.ks = reinterpret_cast<float*>(smem + Y::KS_OFF);
     sh.vs = reinterpret_cast<float*>(smem + Y::VS_OFF);
+    sh.vl = reinterpret_cast<float*>(smem + Y::VL_OFF);
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Y::BAR_OFF);
     auto take = [&](int n) { uint64_t* r = bar; bar += n; return r; };
     sh.raw_full = take(Y::RS);
@@ -637,11 +646,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                   sf = true;
                 }
               }
+              const float va = fabsf(vscale);
               sh.ks[slot * kTreeBlk + ct] = kscale;
               sh.vs[slot * kTreeBlk + ct] = vscale;
-              // V scales are >= 0: their bit patterns order as the values do (a NaN of the
-              // prefix lies above all of them: it must not set the exponent)
-              const unsigned m = __reduce_max_sync(0xffffffffu, vscale <= 3.4e38f ? __float_as_uint(vscale) : 0u);
+              sh.vl[slot * kTreeBlk + ct] = __log2f(va);
+              // bit patterns order as magnitudes do (a NaN of the prefix lies above all of them)
+              const unsigned m = __reduce_max_sync(0xffffffffu, va <= 3.4e38f ? __float_as_uint(va) : 0u);
               sf = __any_sync(0xffffffffu, sf);
               if (lane == 0) {
                 sh.vmax[slot * 4 + (cw & 1)] = __uint_as_float(m);
@@ -815,12 +825,13 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       }
       const uint32_t* mrow = p.mask + (static_cast<long>(sg.q0) + tok) * p.mask_words;
       const int first = sg.n - sg.L;
-      // m: an integer near the running maximum, raised when weights grow past 2^8 .. 2^13, so that
-      // every factor between two of its values is a power of two and re-basing is exact; ev the
-      // exponent of the largest V scale so far.  P holds e = 2^(x - off), off = m + ev, times the
-      // token's V scale, below 2^14; l and O accumulate in that domain.
+      // P holds e = 2^(x - m) times the token's V scale, l sums e, O accumulates P V.  m is an integer near
+      // the running maximum of x + log2 V scale over what this row sees, raised when P grows past 2^8 ..
+      // 2^13, so that every factor between two of its values is a power of two and re-basing is exact.  The
+      // V scale belongs to the maximum, and only the row's own tokens do: a large scale would otherwise
+      // leave the other tokens' P no bits in fp16, for rows that do not see it or give it no weight.
       float m = -INFINITY, moff = 0.f, l = 0.f;               // moff: m, or 0 before the first score
-      int ev = 0, nfseen = 0;                                 // (PT)
+      int nfseen = 0;
       bool begun = false;
       for (int jj = J + ((J ^ st) & 1); jj < J + sg.j1 - sg.j0; jj += 2) {
         const int j = sg.j0 + jj - J;
@@ -856,34 +867,30 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
             return PT ? *reinterpret_cast<const float4*>(kq + c) : make_float4(qsc, qsc, qsc, qsc);
           };
           const float* vsp = sh.vs + slot * kTreeBlk;
+          const float* vlp = sh.vl + slot * kTreeBlk;
+          float most = kMostSum;
           if constexpr (PT) {
             const float2 v2 = *reinterpret_cast<const float2*>(sh.vmax + slot * 4);
-            const float vmx = fmaxf(v2.x, v2.y);
-            const int e = max(exponent_of(vmx), -100);
-            if (!begun) {
-              ev = e;
-            } else if (e > ev) {
-              // (uniform) a larger V scale than before: l and O into the new domain
-              const float f = pow2i(ev - e);
-              ev = e;
-              l *= f;
-              settle();
-              scale_f32(obase, 8, f);
-            }
+            most = kMostSum * pow2i(min(-exponent_of(fmaxf(v2.x, v2.y)), static_cast<int>(kMostE) - 13));
           }
           float2 lsum = make_float2(0.f, 0.f);
-          const float most = PT ? kMostSum * pow2i(-ev) : kMostSum;
-          // m raised to the next integer above mx for the lanes that ask: l and O (and P of the block's
-          // columns before column c0) into the new domain
-          auto rebase = [&](bool ask, float mx, int c0) {
-            float f = 1.f;
-            if (ask && mx > -INFINITY) {
-              const float mn = ceilf(mx);
-              f = m == -INFINITY ? 0.f : pow2i(static_cast<int>(fmaxf(m - mn, -1000.f)));
+          // the m that the row's largest P so far (log2 top) and largest weight (log2 mx) ask for
+          auto wanted = [&](float top, float mx) {
+            return PT ? fmaxf(ceilf(top), ceilf(mx) - kMostE) : ceilf(top);
+          };
+          // m raised to mn for the lanes that ask: l and O (and P of the block's columns before column c0)
+          // into the new domain (in two steps: l may be large where V scales are small)
+          auto rebase = [&](bool ask, float mn, int c0) {
+            float f0 = 1.f, f1 = 1.f;
+            if (ask) {
+              const int d = m == -INFINITY ? -1000 : static_cast<int>(fmaxf(m - mn, -1000.f));
+              f0 = pow2i(d / 2);
+              f1 = pow2i(d - d / 2);
               m = moff = mn;
             }
-            l *= f;
-            lsum = __fmul2_rn(lsum, make_float2(f, f));
+            l = l * f0 * f1;
+            lsum = make_float2(lsum.x * f0 * f1, lsum.y * f0 * f1);
+            const float f = f0 * f1;
             tc::st_wait();
             if (begun) {
               settle();
@@ -918,6 +925,16 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                 }
                 return fmaxf(m0, m1);
               };
+              auto largest_p = [&]() {                        // log2 of the largest P (before 2^-m)
+                float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                  const float4 v = *reinterpret_cast<const float4*>(vlp + 32 * cc + 2 * i);
+                  m0 = max3(m0, t[i].x + v.x, t[i].y + v.y);
+                  m1 = max3(m1, t[i + 1].x + v.z, t[i + 1].y + v.w);
+                }
+                return fmaxf(m0, m1);
+              };
               if constexpr (!MASKED) {
                 tc::ld32(sbase + 32 * cc, s);
               } else {
@@ -928,14 +945,13 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                   if (!((vis >> (2 * i)) & 1u)) t[i].x = -INFINITY;
                   if (!((vis >> (2 * i + 1)) & 1u)) t[i].y = -INFINITY;
                 }
-                const float mx = largest();
-                const bool ask = mx > m + kRebase;
-                if (__any_sync(0xffffffffu, ask)) rebase(ask, mx, 32 * cc);
+                const float mx = largest(), top = PT ? largest_p() : mx;
+                const bool ask = top > m + kRebase || (PT && mx > m + (kMostE + kRebase));
+                if (__any_sync(0xffffffffu, ask)) rebase(ask, wanted(top, mx), 32 * cc);
               }
               uint32_t ph[16], pl[HILO ? 16 : 1];
               auto weights = [&]() {
-                const float off = PT ? moff + static_cast<float>(ev) : moff;
-                const float2 noff = make_float2(-off, -off);
+                const float2 noff = make_float2(-moff, -moff);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -968,14 +984,19 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
               };
               float2 sum = weights();
               if constexpr (!MASKED) {
-                // every column is visible: the maximum need not be known as long as the 32 weights (less
-                // their 2^-ev) sum to no more than 2^13: P then stays inside fp16.  It is found, from
-                // the scores again, for a row's first columns and when that fails.
+                // every column is visible: the maximum need not be known as long as the 32 weights, times
+                // the block's largest V scale, sum to no more than 2^13 (2^14 where the scale is next to
+                // twice its power of two): P then stays inside fp16.  It is found, from the scores
+                // again, for a row's first columns and when that fails.
                 const bool ask = sum.x + sum.y > most || m == -INFINITY;
                 if (__any_sync(0xffffffffu, ask)) {
                   load();
-                  rebase(ask, largest(), 32 * cc);
-                  sum = weights();
+                  const float mx = largest(), mn = wanted(PT ? largest_p() : mx, mx);
+                  const bool raise = ask && mn > m;
+                  if (__any_sync(0xffffffffu, raise)) {
+                    rebase(raise, mn, 32 * cc);
+                    sum = weights();
+                  }
                 }
               }
               lsum = __fadd2_rn(lsum, sum);
@@ -1008,7 +1029,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       ++unit;
       if (!ok) break;
       tc::fence_after_sync();
-      ex[(2 * st) * 128 + r] = moff + static_cast<float>(ev);
+      ex[(2 * st) * 128 + r] = moff;
       ex[(2 * st + 1) * 128 + r] = l;
       if (threadIdx.x < 2) exf[threadIdx.x] = 0;
       ok = sync8();
@@ -1022,7 +1043,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       const bool has0 = l0 != 0.f, has1 = l1 != 0.f;
       const float off = has0 && has1 ? fmaxf(o0, o1) : has0 ? o0 : has1 ? o1 : -INFINITY;
       const float w0 = has0 ? ex2(o0 - off) : 0.f, w1 = has1 ? ex2(o1 - off) : 0.f;
-      const float lt = (has0 ? l0 * w0 : 0.f) + (has1 ? l1 * w1 : 0.f);
+      const float lt = (has0 ? times_2(l0, o0 - off) : 0.f) + (has1 ? times_2(l1, o1 - off) : 0.f);
       const bool whole = sg.j0 == 0 && sg.j1 == sg.nblk;
       float vmul = 1.f;
       if (p.mode == KVQ_SCALE_PER_HEAD) vmul = p.v_static[sg.kvh];
@@ -1166,12 +1187,12 @@ __global__ void __launch_bounds__(256, N == 16 ? 2 : 4) tree_merge_kernel(TreePa
       mx = __shfl_sync(0xffffffffu, mx, 0);
       if (mx > M) {
         const float f = M == -INFINITY ? 0.f : ex2(M - mx);
+        L = M == -INFINITY ? 0.f : times_2(L, M - mx);
         M = mx;
-        L *= f;
         acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
       }
       const float w = ml.y != 0.f ? ex2(mk - M) : 0.f;
-      if (ml.y != 0.f) L = fmaf(ml.y, w, L);
+      if (ml.y != 0.f) L += times_2(ml.y, mk - M);
 #pragma unroll
       for (int t = 0; t < N; ++t) {
         const float wt = __shfl_sync(0xffffffffu, w, t);

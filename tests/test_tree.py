@@ -399,6 +399,94 @@ def test_nonfinite_drafted_rows_reach_only_those_that_see_them(cd, mode, D, valu
         assert not torch.isfinite(vg[3])
 
 
+def crowd(gc, w, q, sees, od, copies=300):
+    """One sequence's tree `copies` times over the same pages, so that most CTAs hold whole units: every
+    copy's output, [copies, L, Hq, D]."""
+    L = q.shape[0]
+    out = gc.tree_attention(q.repeat(copies, 1, 1).cuda(), (torch.arange(copies + 1, dtype=torch.int32) * L).cuda(), L,
+                            pack(sees, (L + 31) // 32).repeat(copies, 1).cuda(), w.block_tables.repeat(copies, 1).cuda(),
+                            w.context_lens.repeat(copies).cuda(), w.max_context, out_dtype=od)
+    return out.view(copies, *q.shape)
+
+
+def hide(sees, starts, b, j):
+    """No query of sequence b sees its drafted token j."""
+    for i in range(int(starts[b]), int(starts[b + 1])):
+        sees[i] = [t for t in sees[i] if t != j]
+
+
+@gpu
+@pytest.mark.parametrize("cd,act,od", [("int8", "bf16", B16), ("int8", "fp16", F32), ("fp8", "bf16", F32), ("fp8", "bf16", B16)])
+@pytest.mark.parametrize("ratio", [2.0 ** 12, 2.0 ** 14, 2.0 ** 20, 1e30])
+def test_hidden_drafted_rows_of_any_size_reach_nobody(cd, act, od, ratio):
+    """Drafted rows that no query sees hold V `ratio` times the others' (per-token scales): the result is
+    that of the rows which are seen."""
+    if act == "fp16" and ratio > 2.0 ** 12:
+        ratio = 2.0 ** 12 if ratio < 2.0 ** 20 else 2.0 ** 14      # (65504 is the largest V that fp16 holds)
+    lens, sizes = [140, 64, 700], [13, 64, 9]
+    w, q, starts, sees, mask, most = make(cd, "per_token_head", act, 8, 2, 128, 16, lens, sizes)
+    for b, j in ((0, 4), (1, 0), (1, 63), (2, 8)):
+        hide(sees, starts, b, j)
+        row = int(w.seq_start[b]) + lens[b] - sizes[b] + j
+        w.v[row] = (w.v[row].float().clamp(-3.9, 3.9) * ratio).to(w.v.dtype)
+    mask = pack(sees, mask.shape[1])
+    oc, gc = helpers.oracle_cache(w), helpers.gpu_cache(w)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    check(run(gc, w, q, starts, mask, most, od), want, spread, od)
+
+
+@gpu
+@pytest.mark.parametrize("cd,od", [("int8", B16), ("int8", F32), ("fp8", B16), ("fp8", F32)])
+@pytest.mark.parametrize("fill", [0x5A, 0xDA, 0xFF, 0x7F, 0x00])
+def test_padding_that_was_never_written(cd, od, fill):
+    """A tree padded to a fixed size whose padding went to slot -1 and is masked for everyone: its K, V and
+    scales are whatever the page held (1.5e16, -3e16, NaN, 3.4e38, 0)."""
+    lens, sizes = [140, 64, 33], [40, 64, 7]
+    w, q, starts, sees, mask, most = make(cd, "per_token_head", "bf16", 8, 2, 128, 16, lens, sizes)
+    for b, pad in ((0, 15), (1, 40), (2, 2)):
+        for j in range(sizes[b] - pad, sizes[b]):
+            hide(sees, starts, b, j)
+            w.slot_mapping[int(w.seq_start[b]) + lens[b] - sizes[b] + j] = -1
+    mask = pack(sees, mask.shape[1])
+    oc, gc = helpers.oracle_cache(w), helpers.gpu_cache(w, fill=fill)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    check(run(gc, w, q, starts, mask, most, od), want, spread, od)
+    assert gc.read_fault() == (0, 0)
+
+
+@gpu
+@pytest.mark.parametrize("cd,od", [("int8", B16), ("int8", F32), ("fp8", B16), ("fp8", F32)])
+@pytest.mark.parametrize("at,ratio", [(5, 2.0 ** 12), (5, 2.0 ** 16), (5, 1e30), (333, 2.0 ** 16), (333, 1e30), (580, 1e30)])
+def test_large_values_of_no_weight(cd, od, at, ratio):
+    """A visible position of the prefix whose V is `ratio` times the others' and whose score lies 200 powers
+    of two below theirs weighs nothing, and takes no bits from those that do."""
+    n, L, D = 600, 4, 128
+    w, q, starts, sees, mask, most = make(cd, "per_token_head", "bf16", 4, 1, D, 16, [n], [L], seed=7)
+    d = torch.randn(D, generator=torch.Generator().manual_seed(9)).sign() / D ** 0.5
+    q = (q.float() * 0.01 + 8.0 * d).to(q.dtype)
+    w.k[at] = (-d * 200).to(w.k.dtype)
+    w.v[at] = (w.v[at].float() * ratio).to(w.v.dtype)
+    oc, gc = helpers.oracle_cache(w), helpers.gpu_cache(w)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    check(crowd(gc, w, q, sees, od), want, spread, od)
+
+
+@gpu
+@pytest.mark.parametrize("low,high", [(-84, 0), (0, 84), (-84, 84)])
+def test_value_scales_of_every_size(low, high):
+    """V of one size in the first half of the context and of another in the second, in either order: the ends
+    of the range that the header names."""
+    n, L = 800, 5
+    for a, b in ((low, high), (high, low)):
+        w, q, starts, sees, mask, most = make("int8", "per_token_head", "bf16", 4, 1, 128, 16, [n], [L], seed=8)
+        size = torch.where(torch.arange(n) < n // 2, 2.0 ** (a + 7), 2.0 ** (b + 5)).view(n, 1, 1)
+        w.v = (w.v.float() * size).to(w.v.dtype)
+        oc, gc = helpers.oracle_cache(w), helpers.gpu_cache(w)
+        want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+        for od in (F32, B16):
+            check(crowd(gc, w, q, sees, od), want, spread, od)
+
+
 @gpu
 def test_two_streams_graph_and_backgrounds():
     """Two calls at once with workspaces of their own, and a captured one replayed on other inputs."""
