@@ -560,9 +560,12 @@ kvq_status kvq_tree_workspace_size(const kvq_cache_desc* cache, int batch, int n
  *   kvq_decode_attention's.  With per-token scales the V scales that a query sees may lie anywhere from
  *   2^-84 to 2^84 (rows with smaller ones lose bits).
  *   Dense caches.  head_dim 128 with block_size 16 (not PER_CHANNEL) runs on the 5th-generation
- *   tensor cores, any GQA group; other geometries on a CUDA-core kernel.  With BF16 output and
- *   8-bit or FP16 caches the tensor-core kernel rounds the probabilities to fp16 (2^-11 relative
- *   at most, an eighth of the output's own half step); otherwise they keep 16 bits or more.
+ *   tensor cores, any GQA group; other geometries on a CUDA-core kernel.  The tensor-core kernel rounds
+ *   the probabilities (not their sum): to fp16 with BF16 output and 8-bit or FP16 caches (2^-11 relative at
+ *   most, an eighth of the output's own half step), to a pair of fp16 with other outputs (2^-22), to a
+ *   pair of bf16 over BF16 caches (2^-17).  With fp16 that is relative or, where larger, absolute: 2^-31
+ *   of the query's largest probability (per-token scales: 2^-29 of its largest product of
+ *   probability and V scale), which probabilities more than 2^18 below the largest meet.
  *   There, batch x kv heads x blocks of 64 positions of max_context (x rows of four tiles of 128
  *   query rows) has to stay below 2^27: KVQ_ERR_UNSUPPORTED.
  *   INT4 / INT2: KVQ_ERR_UNSUPPORTED (a rejected draft could not be taken back out of the ring).

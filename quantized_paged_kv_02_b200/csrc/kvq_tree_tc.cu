@@ -41,8 +41,9 @@
 //
 // Rounding: K and V codes are exact in fp16, q is exact in fp16 (bf16 activations: scaled by a
 // power of two per tile).  P is one fp16 (11 bits) when the output is bf16 (8 bits) and the
-// tiles are fp16, which leaves the output's own rounding ten times larger than P's; otherwise
-// P is a hi + lo pair of 16-bit halves (two MMAs).  Scores, sums and O are binary32.
+// tiles are fp16, which leaves the output's own rounding eight times larger than P's; otherwise
+// P is a hi + lo pair of 16-bit halves (two MMAs; 22 bits in fp16, 17 in bf16).  fp16 has a smallest step besides,
+// 2^-24: half of it is the absolute part of P's error (Range, below).  Scores, sums and O are binary32.
 #include <algorithm>
 #include <climits>
 #include <mutex>
@@ -64,8 +65,20 @@ constexpr int kNS = 3;               // score buffers: one in use per stream, on
 // (16-bit caches: once P V of block J - 6) is complete, which came after P V of block J - 5 (J - 6),
 // hence after the softmax of all blocks up to that: the slot of block J - 8 is free
 constexpr int kNQ = 8;
-constexpr float kRebase = 8.f;       // log2 headroom before the running maximum is re-based,
-constexpr float kMostSum = 8192.f;   // or the sum of 32 weights, times the block's largest V scale, that asks for it
+// Where a row's P lies.  Re-basing puts its largest at 2^PLACE at most; log2 P above LIMIT, or 32 weights that sum
+// (times the block's largest V scale) to more than SUM, ask for it.  fp16 tiles use the whole of
+// fp16's range: what is placed high leaves the smallest weights, behind one position that takes nearly all, bits of
+// their own (half a step, 2^-25, is 2^-31 of the largest; with the largest at 1 a sink of no value and 4000
+// positions 2^18 below it came out further off than 2^-10 of them).  Higher still, what later positions
+// exceed the largest by asks for re-basing more often (ragged FP8: 232 us at 2^5, 235 at 2^7, 242 at 2^9).  Per-token
+// scales stay lower, since SUM holds for the block's largest V scale and may overstate P.  bf16 tiles have
+// the range of binary32.
+template <bool BF, bool PT>
+struct Range {
+  static constexpr float PLACE = BF ? 0.f : PT ? 5.f : 7.f;
+  static constexpr float LIMIT = BF ? 8.f : 15.5f;
+  static constexpr float SUM = BF ? 8192.f : PT ? 32500.f : 65000.f;    // (65504 is the largest fp16)
+};
 constexpr float kMostE = 90.f;       // log2 of the weights themselves stays below about this (V scales below 1)
 // TMEM columns: scores / P of block J in [64 (J % 3), +64), Q in [192, 256), O of stream s in
 // [256 + 128 s, +128)
@@ -826,8 +839,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       const uint32_t* mrow = p.mask + (static_cast<long>(sg.q0) + tok) * p.mask_words;
       const int first = sg.n - sg.L;
       // P holds e = 2^(x - m) times the token's V scale, l sums e, O accumulates P V.  m is an integer near
-      // the running maximum of x + log2 V scale over what this row sees, raised when P grows past 2^8 ..
-      // 2^13, so that every factor between two of its values is a power of two and re-basing is exact.  The
+      // the running maximum of x + log2 V scale over what this row sees, less PLACE, raised when P outgrows
+      // its range, so that every factor between two of its values is a power of two and re-basing is exact.  The
       // V scale belongs to the maximum, and only the row's own tokens do: a large scale would otherwise
       // leave the other tokens' P no bits in fp16, for rows that do not see it or give it no weight.
       float m = -INFINITY, moff = 0.f, l = 0.f;               // moff: m, or 0 before the first score
@@ -868,15 +881,16 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
           };
           const float* vsp = sh.vs + slot * kTreeBlk;
           const float* vlp = sh.vl + slot * kTreeBlk;
-          float most = kMostSum;
+          using Rg = Range<BF, PT>;
+          float most = Rg::SUM;
           if constexpr (PT) {
             const float2 v2 = *reinterpret_cast<const float2*>(sh.vmax + slot * 4);
-            most = kMostSum * pow2i(min(-exponent_of(fmaxf(v2.x, v2.y)), static_cast<int>(kMostE) - 13));
+            most = Rg::SUM * pow2i(min(-exponent_of(fmaxf(v2.x, v2.y)), static_cast<int>(kMostE) - 15));
           }
           float2 lsum = make_float2(0.f, 0.f);
           // the m that the row's largest P so far (log2 top) and largest weight (log2 mx) ask for
           auto wanted = [&](float top, float mx) {
-            return PT ? fmaxf(ceilf(top), ceilf(mx) - kMostE) : ceilf(top);
+            return PT ? fmaxf(ceilf(top) - Rg::PLACE, ceilf(mx) - kMostE) : ceilf(top) - Rg::PLACE;
           };
           // m raised to mn for the lanes that ask: l and O (and P of the block's columns before column c0)
           // into the new domain (in two steps: l may be large where V scales are small)
@@ -946,7 +960,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                   if (!((vis >> (2 * i + 1)) & 1u)) t[i].y = -INFINITY;
                 }
                 const float mx = largest(), top = PT ? largest_p() : mx;
-                const bool ask = top > m + kRebase || (PT && mx > m + (kMostE + kRebase));
+                const bool ask = top > m + Rg::LIMIT || (PT && mx > m + (kMostE + 8.f));
                 if (__any_sync(0xffffffffu, ask)) rebase(ask, wanted(top, mx), 32 * cc);
               }
               uint32_t ph[16], pl[HILO ? 16 : 1];
@@ -985,14 +999,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
               float2 sum = weights();
               if constexpr (!MASKED) {
                 // every column is visible: the maximum need not be known as long as the 32 weights, times
-                // the block's largest V scale, sum to no more than 2^13 (2^14 where the scale is next to
-                // twice its power of two): P then stays inside fp16.  It is found, from the scores
-                // again, for a row's first columns and when that fails.
+                // the block's largest V scale, sum to no more than SUM: P then stays inside fp16.  It is
+                // found, from the scores again, for a row's first columns and when that fails.
                 const bool ask = sum.x + sum.y > most || m == -INFINITY;
                 if (__any_sync(0xffffffffu, ask)) {
                   load();
                   const float mx = largest(), mn = wanted(PT ? largest_p() : mx, mx);
-                  const bool raise = ask && mn > m;
+                  // (every row that has grown, not only those that ask: fewer times in all, 242 against 255 us
+                  // in the ragged FP8 case above)
+                  const bool raise = mn > m;
                   if (__any_sync(0xffffffffu, raise)) {
                     rebase(raise, mn, 32 * cc);
                     sum = weights();

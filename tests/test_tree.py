@@ -488,6 +488,36 @@ def test_value_scales_of_every_size(low, high):
 
 
 @gpu
+@pytest.mark.parametrize("cd,mode,act", [("int8", "per_token_head", "bf16"), ("int8", "per_head", "bf16"), ("fp8", "per_head", "fp16"),
+                                         ("fp16", "none", "fp16"), ("bf16", "none", "bf16")])
+@pytest.mark.parametrize("gap", [14, 18, 22, 30])
+@pytest.mark.parametrize("at", [0, 2000])
+def test_a_sink_of_no_value(cd, mode, act, gap, at):
+    """One position of nearly all the weight whose V is 0, and 4000 others 2^gap below it with one sign in V:
+    the result is what those say, so their weights' roundings add up instead of cancelling."""
+    n, L, D = 4000, 3, 128
+    w, q, starts, sees, mask, most = make(cd, mode, act, 2, 1, D, 16, [n], [L], seed=11)
+    d = torch.randn(D, generator=torch.Generator().manual_seed(9)).sign() / D ** 0.5
+    q = (0.0 * q.float() + 8.0 * d).to(q.dtype)
+    unit = D ** 0.5 / (8.0 * 1.4426950408889634)                   # a key d * unit * x scores x (base-2 units)
+    w.k[:] = (d * unit * 0.4).to(w.k.dtype)
+    w.k[at] = (d * unit * (gap + 0.4)).to(w.k.dtype)
+    w.v = (1 + 0.1 * w.v.float().clamp(-4, 4)).to(w.v.dtype)
+    w.v[at] = 0
+    static = helpers.oracle_static_scales(w)
+    oc, gc = helpers.oracle_cache(w, static), helpers.gpu_cache(w, static=static)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    for od in (F32, B16):
+        got = crowd(gc, w, q, sees, od)
+        # the absolute part of the bound: 2^-31 of the largest weight per position, where scales are not per token
+        # and the others lie more than 2^18 below it
+        floor = 2.0 ** -31 * n * 1.5 / (1 + n * 2.0 ** -gap) if gap > 18 and (mode == "per_head" or cd == "fp16") else 0.0
+        eps = 0.0 if od == F32 else torch.finfo(od).eps / 2
+        err = np.abs(helpers.np64(got) - want)
+        assert (err <= 2.0 ** -10 * spread + eps * np.abs(want) + floor).all(), float((err / spread).max())
+
+
+@gpu
 def test_two_streams_graph_and_backgrounds():
     """Two calls at once with workspaces of their own, and a captured one replayed on other inputs."""
     w, q, starts, sees, mask, most = make("int8", "per_token_head", "bf16", 16, 2, 128, 16, [3000, 1200, 64], [16, 3, 9])
