@@ -964,13 +964,14 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                 if (__any_sync(0xffffffffu, ask)) rebase(ask, wanted(top, mx), 32 * cc);
               }
               uint32_t ph[16], pl[HILO ? 16 : 1];
-              auto weights = [&]() {
+              // from the scores in t, or (blocks that every row sees) straight from S
+              auto weights = [&](auto scaled) {
                 const float2 noff = make_float2(-moff, -moff);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                   float2 a, b;
-                  if constexpr (MASKED) {
+                  if constexpr (decltype(scaled)::value) {
                     a = __fadd2_rn(t[i], noff);
                     b = __fadd2_rn(t[i + 1], noff);
                   } else {
@@ -996,7 +997,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                 }
                 return sum;
               };
-              float2 sum = weights();
+              float2 sum = weights(masked);
               if constexpr (!MASKED) {
                 // every column is visible: the maximum need not be known as long as the 32 weights, times
                 // the block's largest V scale, sum to no more than SUM: P then stays inside fp16.  It is
@@ -1008,10 +1009,10 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
                   // (every row that has grown, not only those that ask: fewer times in all, 242 against 255 us
                   // in the ragged FP8 case above)
                   const bool raise = mn > m;
-                  if (__any_sync(0xffffffffu, raise)) {
-                    rebase(raise, mn, 32 * cc);
-                    sum = weights();
-                  }
+                  if (__any_sync(0xffffffffu, raise)) rebase(raise, mn, 32 * cc);
+                  // (from t, whose largest m was made of: S times the factor less m, rounded once, leaves
+                  // ulp(x) / 2 there, which is more than fits an exponent once scores reach 2^31)
+                  sum = weights(std::true_type{});
                 }
               }
               lsum = __fadd2_rn(lsum, sum);

@@ -518,6 +518,34 @@ def test_a_sink_of_no_value(cd, mode, act, gap, at):
 
 
 @gpu
+@pytest.mark.parametrize("cd,mode,act", [("int8", "per_token_head", "bf16"), ("fp8", "per_head", "bf16"), ("bf16", "none", "bf16")])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 36, 1e30])
+def test_scores_beyond_an_exponents_range(cd, mode, act, size):
+    """Scores whose last binary32 bit is worth many powers of two: the largest one's V row is the result.  A
+    score is off by at most 128 * 2^-24 of the magnitudes that it sums, so rows are checked whose largest lies
+    further above the rest than twice that (and by more than 64 powers of two)."""
+    n, L = 330, 3
+    w, q, starts, sees, mask, most = make(cd, mode, act, 4, 1, 128, 16, [n], [L], seed=14)
+    q = (q.float() * size).to(q.dtype)
+    static = helpers.oracle_static_scales(w)
+    oc, gc = helpers.oracle_cache(w, static), helpers.gpu_cache(w, static=static)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    K = oc.gather(w.block_tables[0].numpy(), n)[0][0]
+    clear = np.zeros((L, 4), bool)
+    for i in range(L):
+        at = list(range(n - L)) + [n - L + j for j in sees[i]]
+        for h in range(4):
+            z = np.sort(K[at] @ helpers.np64(q[i, h])) * 128 ** -0.5
+            off = 128 * 2.0 ** -24 * (np.abs(K[at]) @ np.abs(helpers.np64(q[i, h]))).max() * 128 ** -0.5
+            clear[i, h] = z[-1] - z[-2] > 2 * off + 64
+    assert clear.sum() >= 8
+    for od in (F32, B16):
+        got = run(gc, w, q, starts, mask, most, od)
+        assert torch.isfinite(got).all()
+        check(got[torch.from_numpy(clear).to(got.device)], want[clear], spread[clear], od)
+
+
+@gpu
 def test_two_streams_graph_and_backgrounds():
     """Two calls at once with workspaces of their own, and a captured one replayed on other inputs."""
     w, q, starts, sees, mask, most = make("int8", "per_token_head", "bf16", 16, 2, 128, 16, [3000, 1200, 64], [16, 3, 9])
