@@ -556,7 +556,7 @@ kvq_status kvq_tree_workspace_size(const kvq_cache_desc* cache, int batch, int n
  *                 not shared by calls that overlap on the GPU.
  *   Positions on a block id out of range are left out (counted, KVQ_FAULT_BLOCK).  What a drafted row
  *   holds (values of any size, infinities, NaN, the bytes of a slot that was never written) reaches only
- *   the queries that see it.  With one drafted token that sees itself the result is
+ *   the queries that see it, and no query's values reach another query.  With one drafted token that sees itself the result is
  *   kvq_decode_attention's.  With per-token scales the V scales that a query sees may lie anywhere from
  *   2^-84 to 2^84 (rows with smaller ones lose bits).
  *   Dense caches.  head_dim 128 with block_size 16 (not PER_CHANNEL) runs on the 5th-generation

@@ -39,8 +39,8 @@
 // infinities and NaN are left out of the tile and added in the end to the rows that see
 // them.
 //
-// Rounding: K and V codes are exact in fp16, q is exact in fp16 (bf16 activations: scaled by a
-// power of two per tile).  P is one fp16 (11 bits) when the output is bf16 (8 bits) and the
+// Rounding: K and V codes are exact in fp16, and q is (bf16 activations: scaled by a power of two per row;
+// elements below 2^-26 of the row's largest lose bits).  P is one fp16 (11 bits) when the output is bf16 (8 bits) and the
 // tiles are fp16, which leaves the output's own rounding eight times larger than P's; otherwise
 // P is a hi + lo pair of 16-bit halves (two MMAs; 22 bits in fp16, 17 in bf16).  fp16 has a smallest step besides,
 // 2^-24: half of it is the absolute part of P's error (Range, below).  Scores, sums and O are binary32.
@@ -103,13 +103,13 @@ struct Layout {
   static constexpr int VS_OFF = KS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [kNQ][64]: V scales
   static constexpr int VL_OFF = VS_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [kNQ][64]: log2 of V scales
   static constexpr int KQ_OFF = VL_OFF + (PT ? kNQ * kTreeBlk * 4 : 0);   // float [8][64]: a softmax warp's score factors (PT)
-  static constexpr int EX_OFF = KQ_OFF + (PT ? kSoftWarps * kTreeBlk * 4 : 0);   // float [2][2][128], int [4]: a unit's end
+  static constexpr int EX_OFF = KQ_OFF + (PT ? kSoftWarps * kTreeBlk * 4 : 0);   // float [2][2][128], int [4]: a unit's start and end
   static constexpr int WALK_OFF = EX_OFF + 4 * kTreeRows * 4 + 16;        // Walk [warps]
   static constexpr int MISC_OFF = WALK_OFF + (kThreads / 32 + 1) / 2 * 128;
   // vmax [kNQ][4]; nonfinite flags of scales [kNQ][4] and of V rows [NBV][4]; page masks of the raw
-  // ring / tile buffers; pok [kNQ]; amax [8]; schedule [6]; tmem, abort
+  // ring / tile buffers; pok [kNQ]; schedule [6]; tmem, abort
   static constexpr int NPOK = DIRECT ? NBK : RS;
-  static constexpr int WORDS = 8 * kNQ + 4 * NBV + NPOK + kNQ + 8 + 6 + 2;
+  static constexpr int WORDS = 8 * kNQ + 4 * NBV + NPOK + kNQ + 6 + 2;
   static constexpr int BAR_OFF = (MISC_OFF + 4 * WORDS + 7) / 8 * 8;
   static_assert(MISC_OFF % 16 == 0, "vmax is read four at a time");
   static_assert(!DIRECT || NBK == NBV, "16-bit caches fill K and V of a buffer together");
@@ -174,7 +174,7 @@ struct Shared {
   uint64_t *raw_full, *raw_empty, *tile_full, *k_full, *k_free, *v_full, *v_free, *s_full, *s_free, *p_full, *pv_done,
       *q_ready, *o_full, *sync, *fin;
   int *pages, *pok, *snf, *vnf, *sched;
-  float *vmax, *amax, *ks, *vs, *vl;
+  float *vmax, *ks, *vs, *vl;
   uint32_t* tmem;
   volatile int* abort;
 };
@@ -359,8 +359,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     sh.vnf = sh.snf + 4 * kNQ;                               // [NBV][4]
     sh.pages = sh.vnf + 4 * NBV;
     sh.pok = sh.pages + Y::NPOK;
-    sh.amax = reinterpret_cast<float*>(sh.pok + kNQ);        // [8]
-    sh.sched = reinterpret_cast<int*>(sh.amax + 8);          // [6]
+    sh.sched = sh.pok + kNQ;                                 // [6]
     sh.tmem = reinterpret_cast<uint32_t*>(sh.sched + 6);
     sh.abort = reinterpret_cast<volatile int*>(sh.sched + 7);
     sh.ks = reinterpret_cast<float*>(smem + Y::KS_OFF);
@@ -764,7 +763,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     const int r = 32 * quarter + lane;                        // row of the tile (TMEM lane)
     const uint32_t lanes = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t obase = lanes + kTmO + 128 * st;
-    float* ex = reinterpret_cast<float*>(smem + Y::EX_OFF);   // [2][2][128] at a unit's end
+    float* ex = reinterpret_cast<float*>(smem + Y::EX_OFF);   // [2][2][128] at a unit's end, [2][128] at its start
     int* exf = reinterpret_cast<int*>(ex + 512);              // [2] nonfinite drafted rows seen
     int unit = 0, syncs = 0, seen = 0;                        // seen: blocks of this stream
     bool ok = true;
@@ -776,42 +775,56 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       return __all_sync(0xffffffffu, fine);
     };
     while (ok && next_segment()) {
-      const int R = sg.L * p.g - sg.tile * kTreeRows;         // rows of the tile that exist
-      const int x = sg.tile * kTreeRows + r;
-      const bool row_ok = r < R, warp_ok = 32 * quarter < R;
-      const int tok = row_ok ? x / p.g : 0;
-      const long orow = (static_cast<long>(sg.q0) + tok) * p.Hq + static_cast<long>(sg.kvh) * p.g + (x - tok * p.g);
+      // this thread's row, worked out where it is needed from the segment in shared memory (what stays in
+      // registers across the blocks is spilled there)
+      struct Row {
+        bool ok;                                              // it exists
+        long q;                                               // row of q and out
+        const uint32_t* mask;
+      };
+      auto row = [&]() {
+        const Seg& g = walk->g;
+        const int x = g.tile * kTreeRows + r;
+        Row w;
+        w.ok = x < g.L * p.g;
+        const int tok = w.ok ? x / p.g : 0;
+        const long at = static_cast<long>(g.q0) + tok;
+        w.q = at * p.Hq + static_cast<long>(g.kvh) * p.g + (x - tok * p.g);
+        w.mask = p.mask + at * p.mask_words;
+        return w;
+      };
+      const bool warp_ok = 32 * quarter < sg.L * p.g - sg.tile * kTreeRows;
       // --- this row's q, channels [64 st, 64 st + 64), to tensor memory
       float qsc = p.scale_log2;
+      int notes = 0;                                        // (uniform) bit 0: drafted rows with infinities or NaN; 1: rows of unlike qsc
       {
         if (p.mode == KVQ_SCALE_PER_HEAD) qsc *= p.k_static[sg.kvh];
         if (p.mode == KVQ_SCALE_PER_TENSOR) qsc *= p.k_static[0];
         uint4 u[8];
+        const Row mine = row();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          u[i] = row_ok ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow * kD + 64 * st)[i]
+          u[i] = mine.ok ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + mine.q * kD + 64 * st)[i]
                         : make_uint4(0, 0, 0, 0);
         if constexpr (!BF) {
           if (!p.act_fp16) {
-            // bf16 activations in fp16 tiles: the tile's largest |q| sets a power of two that
-            // keeps every value in range (exact: bf16 has fewer bits than fp16)
+            // bf16 activations in fp16 tiles: a power of two brings each row's largest |q| to 2^13 .. 2^14, so
+            // that elements down to 2^-27 of it keep all their bits (bf16 has fewer than fp16).  A row takes
+            // the one of the warp's largest row where that loses nothing (its own largest is then 2 or
+            // more: 2^-15 of it whole, the rest within 2^-26 of it), its own where the rows differ by more.
             __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(reinterpret_cast<const __nv_bfloat162*>(&u[i])[e]));
-            float amax = fmaxf(__low2float(top), __high2float(top));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            if (lane == 0) sh.amax[warp] = amax;
+            ex[st * kTreeRows + r] = fmaxf(__low2float(top), __high2float(top));   // (64 of 128 channels)
             ok = sync8();
             if (!ok) break;
-            amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < kSoftWarps; ++i) amax = fmaxf(amax, sh.amax[i]);
-            int eq = 0;
-            // (values below 2^-87 of no weight in any score may become 0)
-            if (amax > 0.f && amax <= 3.4e38f) eq = max(exponent_of(amax) - 13, -100);
+            const float amax = fmaxf(ex[r], ex[kTreeRows + r]);
+            const bool usable = amax > 0.f && amax <= 3.4e38f;
+            int eq = usable ? max(exponent_of(amax) - 13, -100) : -100;
+            const int most = __reduce_max_sync(0xffffffffu, eq);
+            if (!usable || eq >= most - 12) eq = most;        // (a row with an infinity sets no other row's)
             const float down = pow2i(-eq);
             qsc *= pow2i(eq);
 #pragma unroll
@@ -825,6 +838,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         }
         const uint32_t flip = qsc < 0.f ? 0x80008000u : 0u;   // a negative static scale: in q's sign
         qsc = fabsf(qsc);
+        if (PT && !__all_sync(0xffffffffu, qsc == __shfl_sync(0xffffffffu, qsc, 0))) notes = 2;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const uint32_t w[8] = {u[i].x ^ flip, u[i].y ^ flip, u[i].z ^ flip, u[i].w ^ flip,
@@ -836,7 +850,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         __syncwarp();
         if (lane == 0) mbar_arrive(sh.q_ready);
       }
-      const uint32_t* mrow = p.mask + (static_cast<long>(sg.q0) + tok) * p.mask_words;
       const int first = sg.n - sg.L;
       // P holds e = 2^(x - m) times the token's V scale, l sums e, O accumulates P V.  m is an integer near
       // the running maximum of x + log2 V scale over what this row sees, less PLACE, raised when P outgrows
@@ -844,7 +857,6 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       // V scale belongs to the maximum, and only the row's own tokens do: a large scale would otherwise
       // leave the other tokens' P no bits in fp16, for rows that do not see it or give it no weight.
       float m = -INFINITY, moff = 0.f, l = 0.f;               // moff: m, or 0 before the first score
-      int nfseen = 0;
       bool begun = false;
       for (int jj = J + ((J ^ st) & 1); jj < J + sg.j1 - sg.j0; jj += 2) {
         const int j = sg.j0 + jj - J;
@@ -854,13 +866,14 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         if (!ok) break;
         tc::fence_after_sync();
         const int pok = sh.pok[slot];
-        const bool fast = j * kTreeBlk + kTreeBlk <= first && pok == kAll;   // uniform
+        // (uniform) every row sees the whole block, and the rows share score factors
+        const bool fast = j * kTreeBlk + kTreeBlk <= first && pok == kAll && notes < 2;
         if (!fast && j * kTreeBlk + kTreeBlk > first) {
           // drafted rows that hold infinities or NaN (the V converters' flags come with the tile)
           const int kb = jj % NBV;
           ok = __all_sync(0xffffffffu, wait(&sh.v_full[kb], (jj / NBV) & 1, sh.abort));
-          nfseen |= sh.vnf[kb * 4] | sh.vnf[kb * 4 + 1] | sh.vnf[kb * 4 + 2] | sh.vnf[kb * 4 + 3];
-          if (PT) nfseen |= sh.snf[slot * 4] | sh.snf[slot * 4 + 1];
+          notes |= sh.vnf[kb * 4] | sh.vnf[kb * 4 + 1] | sh.vnf[kb * 4 + 2] | sh.vnf[kb * 4 + 3];
+          if (PT) notes |= sh.snf[slot * 4] | sh.snf[slot * 4 + 1];
         }
         // this stream's block before: its P V must be complete before O is touched (rare)
         auto settle = [&]() {
@@ -869,8 +882,8 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         };
         if (warp_ok) {
           float* kq = reinterpret_cast<float*>(smem + Y::KQ_OFF) + warp * kTreeBlk;
-          if constexpr (PT) {
-            // each token's score factor, once for the warp's 32 rows: K scale times the tile's
+          if (PT && fast) {
+            // each token's score factor, once for the warp's 32 rows: K scale times theirs
             const float2 f = reinterpret_cast<const float2*>(sh.ks + slot * kTreeBlk)[lane];
             __syncwarp();                                     // (the block before has been read)
             reinterpret_cast<float2*>(kq)[lane] = make_float2(f.x * qsc, f.y * qsc);
@@ -916,16 +929,21 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
           // they came from
           auto block = [&](auto masked) {
             constexpr bool MASKED = decltype(masked)::value;
+            const uint32_t* mrow = MASKED ? row().mask : nullptr;
 #pragma unroll 1
             for (int cc = 0; cc < kTreeBlk / 32; ++cc) {
               uint32_t s[32];
               float2 t[16];
-              // the scores of the 32 columns in the exponent's units
+              // the scores of the 32 columns in the exponent's units (by the row's own factor)
               auto load = [&]() {
                 tc::ld32(sbase + 32 * cc, s);
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                  const float4 f = factor(32 * cc + 2 * i);
+                  float4 f = make_float4(qsc, qsc, qsc, qsc);
+                  if constexpr (PT) {
+                    f = *reinterpret_cast<const float4*>(sh.ks + slot * kTreeBlk + 32 * cc + 2 * i);
+                    f = make_float4(f.x * qsc, f.y * qsc, f.z * qsc, f.w * qsc);
+                  }
                   t[i] = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f.x, f.y));
                   t[i + 1] = __fmul2_rn(make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3])), make_float2(f.z, f.w));
                 }
@@ -1050,7 +1068,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       if (threadIdx.x < 2) exf[threadIdx.x] = 0;
       ok = sync8();
       if (!ok) break;
-      if (nfseen && lane == 0) atomicOr(&exf[0], 1);
+      if ((notes & 1) && lane == 0) atomicOr(&exf[0], 1);
       const float o0 = ex[r], l0 = ex[128 + r], o1 = ex[256 + r], l1 = ex[384 + r];
       ok = sync8();
       if (!ok) break;
@@ -1060,13 +1078,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       const float off = has0 && has1 ? fmaxf(o0, o1) : has0 ? o0 : has1 ? o1 : -INFINITY;
       const float w0 = has0 ? ex2(o0 - off) : 0.f, w1 = has1 ? ex2(o1 - off) : 0.f;
       const float lt = (has0 ? times_2(l0, o0 - off) : 0.f) + (has1 ? times_2(l1, o1 - off) : 0.f);
-      const bool whole = sg.j0 == 0 && sg.j1 == sg.nblk;
+      const Seg& g = walk->g;
+      const Row mine = row();
+      const bool whole = sg.j0 == 0 && sg.j1 == g.nblk;
       float vmul = 1.f;
-      if (p.mode == KVQ_SCALE_PER_HEAD) vmul = p.v_static[sg.kvh];
+      if (p.mode == KVQ_SCALE_PER_HEAD) vmul = p.v_static[g.kvh];
       if (p.mode == KVQ_SCALE_PER_TENSOR) vmul = p.v_static[0];
       const float mul = whole ? (lt != 0.f ? vmul / lt : 0.f) : vmul;
       const long prow = (2L * blockIdx.x + (sg.j0 == 0 ? 1 : 0)) * kTreeRows + r;    // partial row
-      if (!whole && st == 0 && row_ok) *reinterpret_cast<float2*>(p.ws_ml + 2 * prow) = make_float2(off, lt);
+      if (!whole && st == 0 && mine.ok) *reinterpret_cast<float2*>(p.ws_ml + 2 * prow) = make_float2(off, lt);
       if (warp_ok) {
 #pragma unroll 1
         for (int cc = 0; cc < 4; ++cc) {
@@ -1080,15 +1100,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             v[i] = ((has0 ? __uint_as_float(a[i]) * w0 : 0.f) + (has1 ? __uint_as_float(b[i]) * w1 : 0.f)) * mul;
-          if (nonfinite && row_ok) {
+          if (nonfinite && mine.ok) {
             // drafted rows with infinities or NaN in V: their other elements were in the tile; these
             // are added to the rows that see them
             for (int pos = max(first, sg.j0 * kTreeBlk); pos < min(sg.n, sg.j1 * kTreeBlk); ++pos) {
               const int t = pos - first;
-              if (!((mrow[t >> 5] >> (t & 31)) & 1u)) continue;
-              const int blk = p.tables[static_cast<long>(sg.b) * p.max_blocks + pos / kBS];
+              if (!((mine.mask[t >> 5] >> (t & 31)) & 1u)) continue;
+              const int blk = p.tables[static_cast<long>(g.b) * p.max_blocks + pos / kBS];
               if (blk < 0 || blk >= p.NB) continue;
-              const uint8_t* rec = p.pages + (static_cast<long>(blk) * p.H + sg.kvh) * Y::REC;
+              const uint8_t* rec = p.pages + (static_cast<long>(blk) * p.H + g.kvh) * Y::REC;
               const uint8_t* row = rec + Y::OFF_V + (pos % kBS) * Y::ROWB;
               float s = 1.f;
               if constexpr (PT) s = reinterpret_cast<const float*>(rec + Y::OFF_S)[kBS + pos % kBS];
@@ -1103,18 +1123,18 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
               }
             }
           }
-          if (!row_ok) continue;
+          if (!mine.ok) continue;
           if (!whole) {
             float4* dst = reinterpret_cast<float4*>(p.ws_o + prow * kD + d0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           } else if (p.out_dtype == KVQ_DTYPE_FP32) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * kD + d0);
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + mine.q * kD + d0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           } else {
             const bool bf = p.out_dtype == KVQ_DTYPE_BF16;
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow * kD + d0);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + mine.q * kD + d0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t w[4];

@@ -546,6 +546,42 @@ def test_scores_beyond_an_exponents_range(cd, mode, act, size):
 
 
 @gpu
+@pytest.mark.parametrize("cd,mode", [("int8", "per_token_head"), ("fp8", "per_token_head"), ("fp8", "per_head"), ("int8", "per_tensor"),
+                                     ("bf16", "none")])
+@pytest.mark.parametrize("kind", ["large", "inf", "nan", "steps"])
+def test_queries_do_not_reach_each_other(cd, mode, kind):
+    """One tile of query rows (tokens and heads) holds rows of very different size, or one with an infinity or
+    a NaN: every other row's result is its own."""
+    L, hq = 12, 4
+    w, q, starts, sees, mask, most = make(cd, mode, "bf16", hq, 1, 128, 16, [500], [L], seed=12)
+    w.k[:, :, 9] = 0                                                 # (a channel where a query may be anything)
+    bad = []
+    if kind == "large":
+        q[3, 1] *= 1e30
+        bad = [(3, 1)]                                               # (scores of 1e30: some one position's V)
+    elif kind == "steps":                                            # 2^-2 .. 2^-60 of the first
+        q = (q.float() * 2.0 ** (-torch.arange(L).float() * 5 - 2).view(L, 1, 1)).to(q.dtype)
+        q[0, 2] *= 16
+    else:
+        q[3, 1, 7] = float(kind)
+        q[5, 0, 9] = 2.0 ** 20
+        bad = [(3, 1)]
+    static = helpers.oracle_static_scales(w)
+    oc, gc = helpers.oracle_cache(w, static), helpers.gpu_cache(w, static=static)
+    clean = q.clone()
+    clean[3, 1] = 0 if kind in ("inf", "nan") else clean[3, 1]
+    want, spread = attention.tree_attention(oc, helpers.np64(clean), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    rest = np.ones((L, hq), bool)
+    for at in bad:
+        rest[at] = False
+    for od in (F32, B16):
+        got = run(gc, w, q, starts, mask, most, od)
+        check(got[torch.from_numpy(rest).to(got.device)], want[rest], spread[rest], od)
+        if kind == "large":
+            assert torch.isfinite(got).all()
+
+
+@gpu
 def test_two_streams_graph_and_backgrounds():
     """Two calls at once with workspaces of their own, and a captured one replayed on other inputs."""
     w, q, starts, sees, mask, most = make("int8", "per_token_head", "bf16", 16, 2, 128, 16, [3000, 1200, 64], [16, 3, 9])
