@@ -107,9 +107,10 @@ struct Layout {
   static constexpr int WALK_OFF = EX_OFF + 4 * kTreeRows * 4 + 16;        // Walk [warps]
   static constexpr int MISC_OFF = WALK_OFF + (kThreads / 32 + 1) / 2 * 128;
   // vmax [kNQ][4]; nonfinite flags of scales [kNQ][4] and of V rows [NBV][4]; page masks of the raw
-  // ring / tile buffers; pok [kNQ]; schedule [6]; tmem, abort
+  // ring / tile buffers; pok [kNQ]; schedule [6]; tmem, abort;
+  // blocks that each producer issued [4]
   static constexpr int NPOK = DIRECT ? NBK : RS;
-  static constexpr int WORDS = 8 * kNQ + 4 * NBV + NPOK + kNQ + 6 + 2;
+  static constexpr int WORDS = 8 * kNQ + 4 * NBV + NPOK + kNQ + 6 + 2 + 4;
   static constexpr int BAR_OFF = (MISC_OFF + 4 * WORDS + 7) / 8 * 8;
   static_assert(MISC_OFF % 16 == 0, "vmax is read four at a time");
   static_assert(!DIRECT || NBK == NBV, "16-bit caches fill K and V of a buffer together");
@@ -173,7 +174,7 @@ __device__ __noinline__ bool walk_next(const TreeParams& p, Walk* walk) {
 struct Shared {
   uint64_t *raw_full, *raw_empty, *tile_full, *k_full, *k_free, *v_full, *v_free, *s_full, *s_free, *p_full, *pv_done,
       *q_ready, *o_full, *sync, *fin;
-  int *pages, *pok, *snf, *vnf, *sched;
+  int *pages, *pok, *snf, *vnf, *sched, *issued;
   float *vmax, *ks, *vs, *vl;
   uint32_t* tmem;
   volatile int* abort;
@@ -362,6 +363,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     sh.sched = sh.pok + kNQ;                                 // [6]
     sh.tmem = reinterpret_cast<uint32_t*>(sh.sched + 6);
     sh.abort = reinterpret_cast<volatile int*>(sh.sched + 7);
+    sh.issued = sh.sched + 8;                                // [4]
     sh.ks = reinterpret_cast<float*>(smem + Y::KS_OFF);
     sh.vs = reinterpret_cast<float*>(smem + Y::VS_OFF);
     sh.vl = reinterpret_cast<float*>(smem + Y::VL_OFF);
@@ -389,7 +391,7 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       mbar_init(&sh.raw_empty[i], 4);
     }
     for (int i = 0; i < NBK; ++i) {
-      mbar_init(&sh.tile_full[i], 1);
+      mbar_init(&sh.tile_full[i], 4);
       mbar_init(&sh.k_full[i], DIRECT ? 1 : 2);
       mbar_init(&sh.k_free[i], 1);
     }
@@ -476,8 +478,9 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
     // ------------------------------------------------------------ producer
     // 16-bit caches: four warps, each with one of a page's four copies (K and V, two column halves:
     // a tensor copy takes about a hundred cycles to issue, and one warp issuing all sixteen of a
-    // block was the bound); the first also announces the bytes and sends for what comes next
+    // block was the bound), each announcing its own bytes; the first also sends for what comes next
     const int part = warp == kProdWarp ? 0 : warp - kConvWarp0 + 1;
+    constexpr int kParts = DIRECT ? 4 : 1;
     bool run = true;
     int buf = 0, round = 0;                                   // of the raw ring / the tiles
     constexpr int RING = DIRECT ? NBK : Y::RSD;
@@ -522,15 +525,15 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
         run = __all_sync(0xffffffffu, ok);
         if (!run) break;
         uint64_t* full = DIRECT ? &sh.tile_full[buf] : &sh.raw_full[buf];
-        if (lane == 0 && part == 0) {
-          sh.pages[buf] = static_cast<int>(vm);
-          mbar_arrive_expect_tx(full, __popc(vm) * Y::REC);
+        if (lane == 0) {
+          if (part == 0) sh.pages[buf] = static_cast<int>(vm);
+          mbar_arrive_expect_tx(full, __popc(vm) * (Y::REC / kParts));
         }
         __syncwarp();
         if (valid) {
           if constexpr (DIRECT) {
-            // 16 rows of K (parts 0, 1) or V (2, 3), one 128-byte half of their 256 bytes.  (A part
-            // may be ahead of the announcement: the phase still waits for that one arrival.)
+            // 16 rows of K (parts 0, 1) or V (2, 3), one 128-byte half of their 256 bytes
+            static_assert(Y::REC == 4 * kBS * 128, "a part's bytes");
             const int y = (blk * p.H + sg.kvh) * (2 * kBS) + (part >> 1) * kBS, hh = part & 1;
             tma_load_2d(smem + (part >> 1 ? Y::V_OFF : Y::K_OFF) + buf * kTile + hh * (kTile / 2) + lane * kBS * 128, &rows, full,
                         128 * hh, y);
@@ -543,11 +546,26 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
       }
     }
     if (!run && lane == 0) fail(p, sh.abort);
-    // every copy issued must land before the CTA may exit (the first part's wait covers all parts)
+    // every copy issued must land before the CTA may exit.  After a wait that ran out the parts may have
+    // stopped at different blocks (by less than the ring, which turns only when all four have filled a
+    // buffer): once all have stopped, the first arrives for those that did not come to a block, whose phase
+    // then ends when the others' bytes are there.
+    if constexpr (DIRECT) {
+      if (lane == 0) sh.issued[part] = J;
+      __syncwarp();
+      asm volatile("bar.sync 1, 128;" ::: "memory");          // (the four parts: no wait above is without a bound)
+    } else {
+      if (lane == 0) sh.issued[0] = J;
+    }
     if (lane == 0 && part == 0) {
-      for (int i = max(0, J - RING); i < J; ++i)
-        if (!mbar_drain(DIRECT ? &sh.tile_full[i % RING] : &sh.raw_full[i % RING], (i / RING) & 1))
-          record_fault(p.fault, KVQ_FAULT_TIMEOUT);
+      int most = 0;
+      for (int k = 0; k < kParts; ++k) most = max(most, sh.issued[k]);
+      for (int i = max(0, most - RING); i < most; ++i) {
+        uint64_t* full = DIRECT ? &sh.tile_full[i % RING] : &sh.raw_full[i % RING];
+        for (int k = 0; k < kParts; ++k)
+          if (sh.issued[k] <= i) mbar_arrive(full);
+        if (!mbar_drain(full, (i / RING) & 1)) record_fault(p.fault, KVQ_FAULT_TIMEOUT);
+      }
     }
   } else if (warp >= kConvWarp0 && warp < kOutWarp) {
     // ------------------------------------------------------------ converters
