@@ -545,7 +545,7 @@ kvq_status kvq_tree_workspace_size(const kvq_cache_desc* cache, int batch, int n
  *                 sequence.  Nothing is implied: a token sees itself only if its own bit is
  *                 set.  Bits past the sequence's drafted tokens are ignored.
  *   context_lens  int32 [batch], device: cached positions of sequence b, the L_b drafted ones
- *                 included; drafted token j is position context_lens[b] - L_b + j.
+ *                 included, at most 2^31 - 256; drafted token j is position context_lens[b] - L_b + j.
  *   out           out_dtype [num_q_tokens][num_q_heads][D], device.  A query that sees nothing
  *                 (no prefix, no bit) gets zeros.  Rows of no sequence are left as they were, and
  *                 so are those of a sequence that is rejected and counted

@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(TreeParams p) {
   const TreeSeq s = tree_seq(p, b, blockIdx.x == 0 && kvh == 0 && tid == 0);
   const int R = s.L * p.g, r0 = tile * kSimtRows;
   if (r0 >= R) return;
-  const int lo = split * p.chunk, hi = min(s.n, lo + p.chunk);
+  const int lo = split * p.chunk, hi = s.n - lo > p.chunk ? lo + p.chunk : s.n;
   for (int e = tid; e < kSimtRows * D; e += kSimtThreads) {
     const int r = r0 + e / D, d = e % D;
     float x = 0.f;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(256) tree_simt_reduce_kernel(TreeParams p) {
   const TreeSeq s = tree_seq(p, b);
   if (i >= s.L * p.Hq) return;
   const long row = static_cast<long>(s.q0) * p.Hq + i;
-  const int S = (s.n + p.chunk - 1) / p.chunk;
+  const int S = (s.n - 1) / p.chunk + 1;
   const float* ml = p.ws_ml + 2 * row * p.splits;
   const float* o = p.ws_o + row * p.splits * p.D;
   float M = -INFINITY;
@@ -196,6 +196,7 @@ void launch_simt_dim(const TreeParams& p, dim3 grid, cudaStream_t s) {
 kvq_status plan_tree(const Geometry& g, int batch, int num_q_heads, int max_tree, int max_context, TreePlan* p) {
   if (low_bit(g.cache_dtype)) return KVQ_ERR_UNSUPPORTED;
   if (max_tree > kTreeMax) return KVQ_ERR_UNSUPPORTED;
+  max_context = std::min(max_context, kTreeContext);
   const int sms = device_sm_count();
   p->g = num_q_heads / g.H;
   p->kernel = tree_tc_supported(g, p->g) ? 1 : 0;
@@ -336,7 +337,7 @@ kvq_status kvq_tree_attention(const kvq_cache_desc* c, const void* q, int num_q_
   p.max_tree = max_tree;
   p.mask_words = mask_words;
   p.max_blocks = max_blocks_per_seq;
-  p.max_context = max_context;
+  p.max_context = std::min(max_context, kTreeContext);
   p.pages = static_cast<const uint8_t*>(c->pages);
   p.k_static = c->k_scales;
   p.v_static = c->v_scales;

@@ -7,6 +7,9 @@
 namespace kvq {
 
 constexpr int kTreeMax = 1024;       // drafted tokens per sequence at most
+// cached positions per sequence at most: positions and the blocks, pages and splits they are rounded up to
+// stay inside 32 bits
+constexpr int kTreeContext = 0x7FFFFF00;
 constexpr int kTreeGroup = 4;        // CTAs that share a walk at most
 constexpr int kTreeRows = 128;       // tensor-core kernel: query rows per tile
 constexpr int kTreeBlk = 64;         // ... and cached tokens per block

@@ -287,6 +287,25 @@ def test_largest_trees():
 
 
 @gpu
+def test_bounds_need_not_be_tight():
+    """max_tree and max_context are upper bounds: the largest ones change no result."""
+    for D, bs, cd in ((128, 16, "int8"), (64, 16, "int8"), (128, 32, "bf16")):
+        mode = "none" if cd == "bf16" else "per_token_head"
+        lens = [1 + i % 60 for i in range(300)]
+        w, q, starts, sees, mask, most = make(cd, mode, "bf16", 2, 2, D, bs, lens, [1 + i % 2 if n > 1 else 1 for i, n in enumerate(lens)])
+        gc = helpers.gpu_cache(w)
+        a = (q.cuda(), starts.cuda())
+        b = (mask.cuda(), w.block_tables.cuda(), w.context_lens.cuda())
+        want = gc.tree_attention(*a, most, *b, w.max_context)
+        # (the tensor-core kernel's schedule counts fewer than 2^27 blocks)
+        far = 2 ** 31 - 1 if D == 64 or bs != 16 else 2 ** 32 // (300 * 2) // 64 * 64 - 64
+        for most_, context in ((32, w.max_context), (most, far), (32, far)):
+            got = gc.tree_attention(*a, most_, *b, context)
+            assert (got - want).abs().max().item() <= 2.0 ** -18 * max(1.0, want.abs().max().item())
+        assert gc.read_fault() == (0, 0)
+
+
+@gpu
 def test_sequences_that_share_pages():
     """Two sequences with one prefix in the same pages."""
     w, q, starts, sees, mask, most = make("fp8", "per_token_head", "bf16", 8, 2, 128, 16, [300, 300], [12, 12])
