@@ -426,7 +426,8 @@ kvq_status kvq_decode_attention_noalloc(const kvq_cache_desc* cache, const void*
  *     (a, b) -> m * (a cos - b sin, b cos + a sin),
  *   (a, b) = (x[p], x[p + rot_dim/2]) for KVQ_ROPE_HALF, (x[2p], x[2p+1]) for
  *   KVQ_ROPE_INTERLEAVED; x[rot_dim..] passes through unchanged (m does not apply to it).
- *   Angles are formed in float64, so positions up to 2^31 keep float32 accuracy.
+ *   Angles are formed in float64, their products' low parts included, so that cosine and sine are the
+ *   nearest float32 (or the next) for any int32 position.
  */
 typedef enum { KVQ_ROPE_HALF = 0, KVQ_ROPE_INTERLEAVED = 1 } kvq_rope_layout;
 

@@ -5,9 +5,9 @@
 //   (a, b) -> (a cos - b sin, b cos + a sin) * m,   m the attention factor of the scaling,
 // with (a, b) = (x[p], x[p + rot/2]) in the half layout and (x[2p], x[2p+1]) in the
 // interleaved one; dimensions from rot on pass through.  The angle is formed in turns, in
-// binary64 (t * f_p / 2 pi, then less its nearest integer), because in binary32 a position of
-// 2^16 already leaves no more than 8 bits below one radian; cosine and sine are rounded to
-// binary32 once.
+// binary64 (t * f_p / 2 pi, less its nearest integer), because in binary32 a position of 2^16
+// already leaves no more than 8 bits below one radian, with the products' low parts, since at 2^31
+// binary64 alone leaves no more than 24 (3e-7 rad).  Cosine and sine are rounded to binary32 once.
 //
 // What bounds it: bytes (16-bit rows in, 16-bit rows and codes out; 3 flops per element), so
 // the work per element is kept below the copy's.  A CTA takes up to four tokens, whose cosines
@@ -160,11 +160,15 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(RopeParams p, int
     }
   }
   for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
-    constexpr double kInvTwoPi = 0.15915494309189533577;
+    // 1 / 2 pi as the sum of two binary64: what turns are left above whole ones is the remainder of
+    // product with the first (one FMA, exact to its last bit) plus the small parts
+    constexpr double kInvTwoPi = 0x1.45f306dc9c883p-3, kInvTwoPiLow = -0x1.6b01ec5417056p-57;
     const int k = i / pairs, f = i - k * pairs;
-    const double turn = static_cast<double>(p.pos[t0 + k]) * p.freqs[f] * kInvTwoPi;
+    const double t = p.pos[t0 + k], w = p.freqs[f], angle = t * w, low = fma(t, w, -angle);
+    const double whole = rint(angle * kInvTwoPi);
+    const double turn = fma(angle, kInvTwoPi, -whole) + fma(angle, kInvTwoPiLow, low * kInvTwoPi);
     double sn, cs;
-    sincospi(2.0 * (turn - rint(turn)), &sn, &cs);
+    sincospi(2.0 * turn, &sn, &cs);
     cosv[k][f] = static_cast<float>(cs * p.mscale);
     sinv[k][f] = static_cast<float>(sn * p.mscale);
   }

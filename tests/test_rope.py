@@ -205,6 +205,31 @@ def test_rope_matches_oracle(T, hq, hk, D, rot, layout, scaling, act):
 
 
 @gpu
+@pytest.mark.parametrize("exponent", [24, 28, 31])
+@pytest.mark.parametrize("pair", [0, 1])
+def test_far_angles_keep_binary32_accuracy(exponent, pair):
+    """Pairs (a, b) = (1, 1) turned to where one half almost vanishes: what is left of a - b is the
+    angle's error and those of cosine and sine, which the 16-bit output resolves.  The angle is good to
+    binary64, so the bound is that of cosine, sine (half a step of values up to 1: 2^-25 each), one product's
+    rounding (2^-25) and the output's."""
+    r = _rope(128, 16, "half", theta=500000.0)
+    f = float(r.freqs[pair])
+    top = 2 ** exponent - 1
+    t = np.arange(top - 4000000, top + 1, dtype=np.int64)
+    turns = t.astype(np.longdouble) * np.longdouble(f) / (2 * np.longdouble("3.14159265358979323846264338327950288"))
+    near = np.abs(turns - np.floor(turns) - np.longdouble(0.125))           # an eighth of a turn: cos = sin
+    t = t[np.argsort(near)[:24]]
+    x = torch.zeros(24, 1, 128, dtype=torch.bfloat16)
+    x[:, 0, pair] = x[:, 0, 8 + pair] = 1.0
+    y = r.apply(torch.from_numpy(t.astype(np.int32)).cuda(), x.cuda())[0].cpu().double().numpy()[:, 0, pair]
+    ang = np.array([oracle_rope.angle(int(p), f) for p in t])
+    want = np.cos(ang) - np.sin(ang)
+    assert np.abs(want).max() < 2.0 ** -14                                   # (of the positions: near enough)
+    err = np.abs(y - want)
+    assert (err <= 3 * 2.0 ** -25 + 2.0 ** -8 * np.abs(want)).all(), float(err.max())
+
+
+@gpu
 def test_rope_takes_fused_rows_in_place_and_gaps():
     """Views into fused projection rows, rotated in place: v and the gap are left alone."""
     r = _rope(128, 128)
