@@ -587,8 +587,8 @@ kvq_status kvq_tree_attention(const kvq_cache_desc* cache, const void* q, int nu
  *                 below L_b = q_start[b+1] - q_start[b].
  *   accepted      int32 [batch], device, in [0, min(L_b, max_accept)].
  *   context_lens  int32 [batch], device: as for kvq_tree_attention (before the commit).
- *   new_lens      int32 [batch], device, or NULL: receives the new context lengths; not
- *                 context_lens itself.
+ *   new_lens      int32 [batch], device, or NULL: receives the new context lengths; overlaps none of
+ *                 the inputs (KVQ_ERR_INVALID_ARG).
  *   Positions behind the new length keep their bytes.  A sequence with a length or count out of
  *   range (KVQ_FAULT_CONTEXT), or whose path is not increasing, leaves its tree or meets a block
  *   id out of range (KVQ_FAULT_TREE), is counted, moves nothing and keeps context_lens[b].

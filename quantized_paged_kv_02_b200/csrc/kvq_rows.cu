@@ -416,7 +416,14 @@ kvq_status kvq_tree_commit(const kvq_cache_desc* c, const int32_t* path, int max
   if (low_bit(g.cache_dtype)) return KVQ_ERR_UNSUPPORTED;
   if (batch == 0) return KVQ_OK;
   if ((max_accept > 0 && path == nullptr) || accepted == nullptr || q_start == nullptr ||
-      block_tables == nullptr || context_lens == nullptr || new_lens == context_lens)
+      block_tables == nullptr || context_lens == nullptr)
+    return KVQ_ERR_INVALID_ARG;
+  // (a sequence's CTAs, one per tile of heads, all read these, while the first writes its new length)
+  const size_t n = static_cast<size_t>(batch) * sizeof(int32_t);
+  if (new_lens != nullptr &&
+      (bytes_overlap(new_lens, n, context_lens, n) || bytes_overlap(new_lens, n, accepted, n) ||
+       bytes_overlap(new_lens, n, q_start, n + sizeof(int32_t)) || bytes_overlap(new_lens, n, path, n * max_accept) ||
+       bytes_overlap(new_lens, n, block_tables, n * max_blocks_per_seq)))
     return KVQ_ERR_INVALID_ARG;
   const CommitParams p{path, accepted, q_start, block_tables, context_lens, new_lens,
                        static_cast<uint8_t*>(c->pages), max_accept, max_blocks_per_seq, batch,

@@ -49,6 +49,21 @@ def test_commit_refusals():
     assert call(d=_desc(cache_dtype=5, scale_mode=4, block_size=64)) == 2
 
 
+def test_commit_lengths_overlap_no_input():
+    """new_lens is written while other CTAs of the same sequence may still read: no input, nor part of one."""
+    at = dict(path=0x10000, acc=0x20000, qs=0x30000, bt=0x40000, lens=0x50000)
+    size = dict(path=4 * 6 * 5, acc=24, qs=28, bt=4 * 6 * 7, lens=24)
+    d, L = _desc(), kvq.lib
+
+    def call(new):
+        p = {k: ctypes.c_void_p(v) for k, v in at.items()}
+        return L.kvq_tree_commit(ctypes.byref(d), p["path"], 5, p["acc"], 6, p["qs"], p["bt"], 7, p["lens"], ctypes.c_void_p(new), None)
+
+    for name, base in at.items():
+        for new in (base, base + 4, base - 20, base + size[name] - 4):
+            assert call(new) == 1, (name, new - base)
+
+
 # ------------------------------------------------------------------------------- GPU
 gpu = pytest.mark.gpu
 DENSE = [("int8", "per_token_head", 16, 128, "bf16"), ("int8", "per_token_head", 5, 64, "fp16"),
