@@ -487,7 +487,8 @@ kvq_status kvq_rope_frequencies(const kvq_rope_desc* rope, double* freqs, double
  *                 elements apart (multiples of 8, at least heads * head_dim: rows of a fused
  *                 projection are taken as they are).  With 0 heads the tensor is not looked at.
  *   q_out, k_out  the same shapes with strides of their own; an output may be its own input
- *                 (same pointer and stride), but may not overlap it otherwise.
+ *                 (same pointer and stride), and otherwise overlaps no input and no other output
+ *                 (KVQ_ERR_INVALID_ARG; columns of one buffer have to share its stride).
  *   Values are rotated in float32 and rounded once to act_dtype.
  */
 kvq_status kvq_rope(const kvq_rope_desc* rope, const double* freqs, int32_t act_dtype, int head_dim,
@@ -517,7 +518,7 @@ kvq_status kvq_rope_write(const kvq_cache_desc* cache, const kvq_rope_desc* rope
  * kvq_gather - read cached rows back by slot (the counterpart of kvq_write).
  *   slots         int32 [num_rows], device: cache slot of each row.  -1 leaves the output row as
  *                 it was, and so does a slot out of range (counted, KVQ_FAULT_SLOT).
- *   k_out, v_out  act_dtype [num_rows][H][D], device: the dequantized values of the header
+ *   k_out, v_out  act_dtype [num_rows][H][D], device, apart from one another: the dequantized values of the header
  *                 comment, formed in float32 and rounded once to act_dtype (16-bit caches: the
  *                 stored bits).
  *   Every cache type; for INT4 / INT2 rows of blocks only (the residual ring has no slots).

@@ -346,6 +346,28 @@ bool rows_ok(const void* p, int64_t stride, int heads, int D) {
   return p != nullptr && aligned(p) && stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * D;
 }
 
+// T rows of `wide` elements each, `stride` elements apart.
+struct Rows {
+  const void* at;
+  int64_t stride, wide;
+};
+
+// Do two tensors of T such rows (16-bit elements) overlap?  Columns of one buffer, which have one stride, lie
+// between one another; tensors of different strides within one range count as overlapping.
+bool rows_overlap(const Rows& a, const Rows& b, int T) {
+  if (!bytes_overlap(a.at, 2 * ((T - 1) * a.stride + a.wide), b.at, 2 * ((T - 1) * b.stride + b.wide))) return false;
+  if (a.stride != b.stride || T == 1) return true;
+  const int64_t s = 2 * a.stride;
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.at) - reinterpret_cast<uintptr_t>(a.at)) % s;
+  const int64_t from = d < 0 ? d + s : d;                    // b's rows begin here in a's period
+  return from < 2 * a.wide || from + 2 * b.wide > s;
+}
+
+// May `out` be written while `in` is read?  As its own input (same rows) or apart from it.
+bool in_place(const Rows& out, const Rows& in, int T) {
+  return (out.at == in.at && out.stride == in.stride) || !rows_overlap(out, in, T);
+}
+
 }  // namespace
 }  // namespace kvq
 
@@ -405,6 +427,13 @@ kvq_status kvq_rope(const kvq_rope_desc* r, const double* freqs, int32_t act_dty
     return KVQ_ERR_INVALID_ARG;
   if (num_kv_heads > 0 && (!rows_ok(k, k_stride, num_kv_heads, head_dim) || !rows_ok(k_out, k_out_stride, num_kv_heads, head_dim)))
     return KVQ_ERR_INVALID_ARG;
+  const int64_t qw = static_cast<int64_t>(num_q_heads) * head_dim, kw = static_cast<int64_t>(num_kv_heads) * head_dim;
+  const Rows rq{q, q_stride, qw}, rqo{q_out, q_out_stride, qw}, rk{k, k_stride, kw}, rko{k_out, k_out_stride, kw};
+  if (num_q_heads > 0 && !in_place(rqo, rq, num_tokens)) return KVQ_ERR_INVALID_ARG;
+  if (num_kv_heads > 0 && !in_place(rko, rk, num_tokens)) return KVQ_ERR_INVALID_ARG;
+  if (num_q_heads > 0 && num_kv_heads > 0 &&
+      (rows_overlap(rqo, rk, num_tokens) || rows_overlap(rko, rq, num_tokens) || rows_overlap(rqo, rko, num_tokens)))
+    return KVQ_ERR_INVALID_ARG;
   p.q = q;
   p.k = k;
   p.q_out = q_out;
@@ -443,6 +472,13 @@ kvq_status kvq_rope_write(const kvq_cache_desc* c, const kvq_rope_desc* r, const
   if (num_q_heads > 0 && (!rows_ok(q, q_stride, num_q_heads, g.D) || !rows_ok(q_out, q_out_stride, num_q_heads, g.D)))
     return KVQ_ERR_INVALID_ARG;
   if (!rows_ok(k_new, k_stride, g.H, g.D) || !rows_ok(v_new, v_stride, g.H, g.D)) return KVQ_ERR_INVALID_ARG;
+  if (num_q_heads > 0) {
+    const int64_t qw = static_cast<int64_t>(num_q_heads) * g.D, kw = static_cast<int64_t>(g.H) * g.D;
+    const Rows out{q_out, q_out_stride, qw};
+    if (!in_place(out, {q, q_stride, qw}, num_tokens) || rows_overlap(out, {k_new, k_stride, kw}, num_tokens) ||
+        rows_overlap(out, {v_new, v_stride, kw}, num_tokens))
+      return KVQ_ERR_INVALID_ARG;
+  }
   p.q = q;
   p.k = k_new;
   p.v = v_new;

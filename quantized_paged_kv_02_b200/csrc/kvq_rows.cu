@@ -395,6 +395,8 @@ kvq_status kvq_gather(const kvq_cache_desc* c, const int32_t* slots, int num_row
   if (num_rows == 0) return KVQ_OK;
   if (slots == nullptr || k_out == nullptr || v_out == nullptr || !aligned(k_out) || !aligned(v_out))
     return KVQ_ERR_INVALID_ARG;
+  const size_t bytes = static_cast<size_t>(num_rows) * g.H * g.D * 2;
+  if (bytes_overlap(k_out, bytes, v_out, bytes)) return KVQ_ERR_INVALID_ARG;
   const GatherParams p{slots, static_cast<const uint8_t*>(c->pages), c->k_scales, c->v_scales, g.NB, g.bs, g.H,
                        g.record, g.off_v, g.off_s, g.row_bytes, g.scale_mode, k_out, v_out, c->fault};
   int shift = -1;

@@ -158,6 +158,52 @@ def test_rope_refusals():
     assert write(desc=lo) == 2
 
 
+def test_outputs_that_overlap_what_is_read_are_refused():
+    """An output may be its own input; any other overlap (k read while q is rotated into it, one output over
+    the other, shifted rows) would race.  Columns of one buffer do not overlap."""
+    r, fake, L = _rope(128, 128, device="cpu").desc, ctypes.c_void_p(0x1000), kvq.lib
+    P = lambda x: ctypes.c_void_p(x)
+    A, B, C = 0x100000, 0x200000, 0x300000
+    T = 5
+
+    def rope(q, qs, qo, qos, k, ks, ko, kos):
+        return L.kvq_rope(ctypes.byref(r), fake, 0, 128, fake, T, P(q), qs, 4, P(qo), qos, P(k), ks, 2, P(ko), kos, None)
+
+    apart = 3 if not torch.cuda.is_available() else None            # (without a GPU the launch fails: KVQ_ERR_CUDA)
+    row = 4 * 128 + 2 * 128                                         # q and k columns of one buffer
+    for bad in ((A, 512, B, 512, B, 256, C, 256),                   # q_out over k
+                (A, 512, A, 512, A, 512, B, 256),                   # in place over what is k too
+                (A, 512, B, 512, C, 256, A + 16, 256),              # k_out inside q
+                (A, 512, B, 512, C, 256, B + 2 * 512 * T - 16, 256),    # ... or in q_out's last bytes
+                (A, 512, A + 256, 512, B, 256, C, 256),             # shifted
+                (A, 512, A, 520, B, 256, C, 256),                   # another stride
+                (A, row, A, row, A + 1008, row, A + 1008, row)):    # columns that share a chunk
+        assert rope(*bad) == 1, bad
+    if apart is not None:
+        assert rope(A, row, A, row, A + 1024, row, A + 1024, row) == apart
+        assert rope(A + 512, row, A + 512, row, A, row, A, row) == apart
+        assert rope(A, 512, B, 512, A, 512, C, 256) == apart        # one tensor as both
+        assert rope(A, 512, B, 512, C, 256, B + 2 * 512 * T, 256) == apart
+
+    d = kvq.CacheDesc()
+    for k, v in dict(cache_dtype=3, act_dtype=0, scale_mode=1, num_blocks=8, block_size=16, num_kv_heads=2, head_dim=128,
+                     pages=0x900000).items():
+        setattr(d, k, v)
+
+    def write(q, qs, qo, qos, k, ks, v, vs):
+        return L.kvq_rope_write(ctypes.byref(d), ctypes.byref(r), fake, fake, T, P(q), qs, 4, P(qo), qos, P(k), ks, P(v), vs, fake, None)
+
+    for bad in ((A, 512, B, 512, B, 256, C, 256), (A, 512, B, 512, C, 256, B + 16, 256), (A, 512, A + 16, 512, B, 256, C, 256)):
+        assert write(*bad) == 1, bad
+    if apart is not None:
+        fused = row + 256
+        assert write(A, fused, A, fused, A + 1024, fused, A + 1536, fused) == apart
+        assert write(A, 512, B, 512, C, 256, C, 256) == apart
+    # rows read back: K and V apart
+    assert L.kvq_gather(ctypes.byref(d), fake, 4, P(A), P(A), None) == 1
+    assert L.kvq_gather(ctypes.byref(d), fake, 4, P(A), P(A + 4 * 512 - 16), None) == 1
+
+
 # ------------------------------------------------------------------------------- GPU
 gpu = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
