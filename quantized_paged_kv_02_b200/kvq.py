@@ -459,6 +459,8 @@ def kvq_tree_attention(desc, q, q_start, max_tree, tree_mask, block_tables, cont
         raise ValueError("q must be contiguous [tokens, heads, %d] of the cache's activation type" % desc.head_dim)
     if out.shape != (T, Hq, D) or not out.is_contiguous():
         raise ValueError("out must be contiguous and have the shape of q")
+    if out.dtype not in _OUT_CODE:
+        raise TypeError("out must be bfloat16, float16 or float32, got %s" % out.dtype)
     B = context_lens.numel()
     if tree_mask.dim() != 2 or block_tables.dim() != 2:
         raise ValueError("tree_mask must be [tokens, words] and block_tables [batch, blocks]")

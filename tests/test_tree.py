@@ -100,6 +100,13 @@ def test_mask_words_hold_the_bits():
         assert [j for j in range(96) if (int(m[i, j // 32]) >> (j % 32)) & 1] == sorted(s)
 
 
+def test_output_type_is_checked():
+    q = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        kvq.kvq_tree_attention(_desc(), q, None, 2, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(1, 4, dtype=torch.int32),
+                               torch.zeros(1, dtype=torch.int32), 64, q.double())
+
+
 def _desc(**kw):
     d = kvq.CacheDesc()
     base = dict(cache_dtype=3, act_dtype=0, scale_mode=1, num_blocks=8, block_size=16, num_kv_heads=2, head_dim=128,
