@@ -288,8 +288,8 @@ __device__ __forceinline__ void prefetch_line(const void* src) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
 }
 
-// O or P columns [base, base + 16 n) of the warp's lanes times a power of two per lane: float32
-// values, or 16-bit pairs (one element's factor in f2).
+// O or P columns [base, base + 16 n) of the warp's lanes times a power of two per lane: float32 values, or
+// 16-bit pairs (f0 f1 may lie below fp16's smallest value where what it leaves of a large P does not).
 __device__ __forceinline__ void scale_f32(uint32_t base, int n, float f) {
 #pragma unroll 1
   for (int c = 0; c < n; ++c) {
@@ -302,7 +302,7 @@ __device__ __forceinline__ void scale_f32(uint32_t base, int n, float f) {
   }
 }
 template <bool BF, bool HILO>
-__device__ __forceinline__ void scale_p(uint32_t base, int n, float f) {
+__device__ __forceinline__ void scale_p(uint32_t base, int n, float f0, float f1) {
 #pragma unroll 1
   for (int c = 0; c < n; ++c) {
     uint32_t r[16];
@@ -310,10 +310,10 @@ __device__ __forceinline__ void scale_p(uint32_t base, int n, float f) {
 #pragma unroll
     for (int i = 0; i < (HILO ? 16 : 8); ++i) {
       if constexpr (BF) {
-        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r[i]), __float2bfloat162_rn(f));
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r[i]), __float2bfloat162_rn(f0 * f1));
         r[i] = *reinterpret_cast<const uint32_t*>(&v);
       } else {
-        const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&r[i]), __float2half2_rn(f));
+        const __half2 v = __hmul2(__hmul2(*reinterpret_cast<__half2*>(&r[i]), __float2half2_rn(f0)), __float2half2_rn(f1));
         r[i] = *reinterpret_cast<const uint32_t*>(&v);
       }
     }
@@ -935,13 +935,12 @@ tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUt
             }
             l = l * f0 * f1;
             lsum = make_float2(lsum.x * f0 * f1, lsum.y * f0 * f1);
-            const float f = f0 * f1;
             tc::st_wait();
             if (begun) {
               settle();
-              scale_f32(obase, 8, f);
+              scale_f32(obase, 8, f0 * f1);
             }
-            scale_p<BF, HILO>(sbase, c0 / 16, f);
+            scale_p<BF, HILO>(sbase, c0 / 16, f0, f1);
           };
           // --- 32 columns at a time: scores times the K scale, e, its sum, and P over the scores
           // they came from

@@ -608,6 +608,37 @@ def test_queries_do_not_reach_each_other(cd, mode, kind):
 
 
 @gpu
+@pytest.mark.parametrize("cd,mode,act", [("int8", "per_head", "bf16"), ("fp8", "per_head", "fp16"), ("fp16", "none", "fp16")])
+@pytest.mark.parametrize("drafted", [False, True])
+def test_a_new_maximum_in_the_second_half_of_a_block(cd, mode, act, drafted):
+    """32 positions, and 2^26 above them one of no value in the same block's second half: the first ones'
+    probabilities, already stored, are scaled by 2^-26 or so, less than the smallest fp16, to what is more."""
+    gap, D = 26, 128
+    n, L = (60, 60) if drafted else (64, 0)
+    n += 0 if drafted else 3
+    L = L or 3
+    w, q, starts, sees, mask, most = make(cd, mode, act, 2, 1, D, 16, [n], [L], seed=15)
+    d = torch.randn(D, generator=torch.Generator().manual_seed(9)).sign() / D ** 0.5
+    q = (0.0 * q.float() + 8.0 * d).to(q.dtype)
+    unit = D ** 0.5 / (8.0 * 1.4426950408889634)
+    w.k[:] = (d * unit * 0.4).to(w.k.dtype)
+    w.k[40] = (d * unit * (gap + 0.4)).to(w.k.dtype)
+    w.v = (1 + 0.1 * w.v.float().clamp(-4, 4)).to(w.v.dtype)
+    w.v[40] = 0
+    sees = [list(range(L)) if drafted else s for s in sees]
+    mask = pack(sees, mask.shape[1])
+    static = helpers.oracle_static_scales(w)
+    oc, gc = helpers.oracle_cache(w, static), helpers.gpu_cache(w, static=static)
+    want, spread = attention.tree_attention(oc, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    for od in (F32, B16):
+        got = run(gc, w, q, starts, mask, most, od)
+        err = np.abs(helpers.np64(got) - want)
+        # 2^-31 of the largest probability (which is 1) per position, as far as fp16 goes
+        eps = 0.0 if od == F32 else torch.finfo(od).eps / 2
+        assert (err <= 2.0 ** -10 * spread + eps * np.abs(want) + 2.0 ** -31 * n * 1.5).all(), float((err / spread).max())
+
+
+@gpu
 def test_two_streams_graph_and_backgrounds():
     """Two calls at once with workspaces of their own, and a captured one replayed on other inputs."""
     w, q, starts, sees, mask, most = make("int8", "per_token_head", "bf16", 16, 2, 128, 16, [3000, 1200, 64], [16, 3, 9])
