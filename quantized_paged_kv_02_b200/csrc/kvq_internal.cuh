@@ -247,12 +247,6 @@ __host__ __device__ inline bool low_bit(int cache_dtype) {
   return cache_dtype == KVQ_DTYPE_INT4 || cache_dtype == KVQ_DTYPE_INT2;
 }
 
-// Do n bytes at a and m bytes at b overlap?
-inline bool bytes_overlap(const void* a, size_t n, const void* b, size_t m) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return n > 0 && m > 0 && x < y + m && y < x + n;
-}
-
 // Launchers implemented in the .cu files; return a cudaError_t from the launch.
 cudaError_t launch_write_dense(const kvq_cache_desc& c, const Geometry& g, const void* k,
                                const void* v, int T, const int32_t* slots, cudaStream_t s);

@@ -27,6 +27,7 @@
 #include <climits>
 #include <cmath>
 
+#include "kvq_checks.cuh"
 #include "kvq_internal.cuh"
 #include "kvq_ptx.cuh"
 

@@ -17,6 +17,7 @@
 // dependent loads (path, table) before a row's bytes can be asked for.
 #include <algorithm>
 
+#include "kvq_checks.cuh"
 #include "kvq_internal.cuh"
 #include "kvq_ptx.cuh"
 
