@@ -370,6 +370,10 @@ kvq_status kvq_append_decode_attention(const kvq_cache_desc* cache, const void* 
  *   each page dequantized once per tile); other groups of up to 8 on the dense tensor-core
  *   decode kernel's per-query mode (dense caches only).  Anything else returns
  *   KVQ_ERR_UNSUPPORTED.
+ *   With per-token scales the 5th-generation kernel holds probabilities times V scales relative to the
+ *   largest V scale of the blocks of 128 positions that a tile of queries has walked, positions behind a
+ *   query included: scales that span more than 2^16 there cost the smaller ones' rows accuracy (error
+ *   6e-4 of values of 0.5 at 2^16, 1e-2 at 2^20).
  */
 kvq_status kvq_prefill_attention(const kvq_cache_desc* cache, const void* q, int num_q_tokens,
                                  int batch, int num_q_heads, const int32_t* q_start,
@@ -558,9 +562,11 @@ kvq_status kvq_tree_workspace_size(const kvq_cache_desc* cache, int batch, int n
  *                 not shared by calls that overlap on the GPU.
  *   Positions on a block id out of range are left out (counted, KVQ_FAULT_BLOCK).  What a drafted row
  *   holds (values of any size, infinities, NaN, the bytes of a slot that was never written) reaches only
- *   the queries that see it, and no query's values reach another query.  With one drafted token that sees itself the result is
- *   kvq_decode_attention's.  With per-token scales the V scales that a query sees may lie anywhere from
- *   2^-84 to 2^84 (rows with smaller ones lose bits).
+ *   the queries that see it, and no query's values reach another query.  An infinity that a query does
+ *   see in the prefix of a 16-bit cache's V leaves that channel infinite or NaN.  With one drafted
+ *   token that sees itself the result is kvq_decode_attention's, up to the roundings below.  With
+ *   per-token scales the V scales that a query sees may lie anywhere from 2^-84 to 2^84 (rows with
+ *   smaller ones may lose bits).
  *   Dense caches.  head_dim 128 with block_size 16 (not PER_CHANNEL) runs on the 5th-generation
  *   tensor cores, any GQA group; other geometries on a CUDA-core kernel.  The tensor-core kernel rounds
  *   the probabilities (not their sum): to fp16 with BF16 output and 8-bit or FP16 caches (2^-11 relative at

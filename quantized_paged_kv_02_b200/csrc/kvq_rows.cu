@@ -11,10 +11,12 @@
 // source, and moving the rows in order, each batch read whole before it is written, never
 // overwrites a row still to be read.  Codes and per-token scales move as bytes.
 //
-// Measured (B200): gather of 2048 tokens x 32 heads INT8 16.4 us, 3.1 TB/s (16 MB in, 34 MB out: start
-// and end of a launch are half of it), 32640 x 8 INT4 rows 49 us, 3.5 TB/s (what four codes cost to
-// unpack is next to the bytes); commit of 256 trees of 64 over 32 bf16 heads 23 us, 3.1 TB/s: two
-// dependent loads (path, table) before a row's bytes can be asked for.
+// Measured (B200, behind an L2 flush / back to back): gather of 32-head INT8 rows 18 / 12 us for 2048 tokens,
+// 45 / 41 for 8192, 141 / 138 for 32640, so some 13 us of start and end and then 1.04 times the bytes' time
+// at copy speed; 32640 x 8 INT4 rows 49 / 47 us, 1.5 times the bytes' time a further row: their unpacking has the
+// issue slots 79% busy, DRAM 28%.  Commit of 256 trees of 64 over 32 bf16 heads 24 / 20 us (10.9 at copy
+// speed): two dependent loads (path, table) before a row's bytes can be asked for, in 2.6 waves of
+// CTAs; DRAM 20% busy.
 #include <algorithm>
 
 #include "kvq_checks.cuh"

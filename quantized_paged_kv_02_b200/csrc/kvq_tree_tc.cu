@@ -20,13 +20,14 @@
 //   warp 9          issues S = Q K^T;  warp 18 issues O += P V;
 //   warps 10-13     K converters, 14-17 V converters: codes -> fp16 tiles (exact), two warps per block.
 //
-// Measured (B200; GB/s of cache read, bf16 results): trees of 16, 64 / 8 heads over 24 x 16384 INT8
-// 309 us, 2.7 TB/s; ragged trees, 32 / 8 heads over 64 x 1024..8192 FP8 233 us, 2.7 TB/s; trees of 64
-// over 8 x 16384 bf16 397 us, 1.4 TB/s and 690 TFLOP/s (hi + lo P: three products for two).  Bytes are
-// not the bound, nor the tensor pipe (31% busy; 47% for bf16): it is instruction issue.  About 6800 warp
-// instructions go into 128 positions (a softmax warp 450 per 64, a converter warp 300 per 64), 52% of
-// the issue slots, and the rest are waits on latencies that 19 warps do not cover.  What follows:
-// scores, weights and sums are packed pairs, blocks that every row sees skip the maximum, two converter
+// Measured (B200, bf16 results; one call behind an L2 flush / seconds of calls back to back, where the
+// 1000 W cap holds the SMs at 1880, 1680 and 1590 MHz of 1965): ragged trees, 32 / 8 heads over 64 x 1024..8192
+// FP8 237 / 240 us; trees of 16, 64 / 8 heads over 24 x 16384 INT8 302 / 342 us (2.8 / 2.5 TB/s of cache);
+// trees of 64 over 8 x 16384 bf16 400 / 471 us (690 / 583 TFLOP/s; hi + lo P: three products for two).  No rate
+// is the bound: DRAM is 31% busy (14% for bf16), the tensor pipe 32% (46%), the issue slots 52% (50%).  It is
+// the latency of a block's chain, from its scores to its weights, that 19 warps of 96 registers do not
+// cover.  About 6700 warp instructions go into 128 positions (a softmax warp 450 per 64, a converter
+// warp 300 per 64).  What follows: scores, weights and sums are packed pairs, blocks that every row sees skip the maximum, two converter
 // warps per block rather than four (331 -> 317 us), and the roles' loops are kept small, since together
 // they have to fit the instruction cache (5% of the time when they did not).  Starting and ending a
 // unit costs 8 us of a CTA, which the shares count.
@@ -39,14 +40,14 @@
 // infinities and NaN are left out of the tile and added in the end to the rows that see
 // them.
 //
-// Rounding: K and V codes are exact in fp16, and q is (bf16 activations: scaled by a power of two per row;
-// elements below 2^-26 of the row's largest lose bits).  P is one fp16 (11 bits) when the output is bf16 (8 bits) and the
-// tiles are fp16, which leaves the output's own rounding eight times larger than P's; otherwise
-// P is a hi + lo pair of 16-bit halves (two MMAs; 22 bits in fp16, 17 in bf16).  fp16 has a smallest step besides,
-// 2^-24: half of it is the absolute part of P's error (Range, below).  Scores, sums and O are binary32.
+// Rounding: K and V codes are exact in fp16, and q is (bf16 activations: scaled by a power of two per
+// row; elements below 2^-26 of the row's largest lose bits).  P is one fp16 (11 bits) when the output is
+// bf16 (8 bits) and the tiles are fp16, which leaves the output's own rounding eight times larger than P's
+// (a pair there costs 306 -> 357 us in the INT8 case above and 239 -> 269 us in the FP8 one; the error against 64 bits,
+// 0.0017 of the output, is that of binary32 probabilities as it is); otherwise P is a hi + lo pair of 16-bit
+// halves (two MMAs; 22 bits in fp16, 17 in bf16).  fp16 has a smallest step besides, 2^-24: half of it is the absolute part of P's error (Range,
+// below).  Scores, sums and O are binary32.
 #include <algorithm>
-#include <climits>
-#include <mutex>
 
 #include "kvq_decode_common.cuh"
 #include "kvq_ptx.cuh"

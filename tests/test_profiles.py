@@ -27,6 +27,14 @@ def test_decode_profile_matches_current_sources(workload):
     assert traffic is not None and traffic > 0
 
 
+def test_tree_profile_matches_current_sources():
+    text = open(os.path.join(ROOT, "profiles", "tree_attention.md")).read()
+    names = re.search(r"kernel_sources:\s*(.+)", text).group(1).split()
+    assert "kvq_tree_tc.cu" in names
+    assert bench.kernel_source_hash(names) == re.search(r"kernel_source_sha256:\s*([0-9a-f]+)", text).group(1), (
+        "profiles/tree_attention.md was captured on other kernel sources; re-take its counters")
+
+
 def test_profiles_hold_text_summaries_only():
     """profiles/ keeps short text summaries (the figures used and the commands that made
     them), never raw reports."""

@@ -639,6 +639,22 @@ def test_a_new_maximum_in_the_second_half_of_a_block(cd, mode, act, drafted):
 
 
 @gpu
+@pytest.mark.parametrize("od", [F32, B16])
+def test_an_infinity_of_the_prefix_stays_in_its_channel(od):
+    """V of a visible prefix position holds an infinity: its channel is infinite or NaN, the others are as they
+    would be without it."""
+    w, q, starts, sees, mask, most = make("bf16", "none", "bf16", 8, 2, 128, 16, [500, 90], [9, 9])
+    clean = helpers.oracle_cache(w)
+    want, spread = attention.tree_attention(clean, helpers.np64(q), starts.numpy(), sees, w.block_tables.numpy(), w.context_lens.numpy())
+    w.v[100, 0, 7], w.v[int(w.seq_start[1]) + 3, 1, 64] = float("inf"), float("-inf")
+    got = run(helpers.gpu_cache(w), w, q, starts, mask, most, od)
+    hit = np.zeros(got.shape, bool)
+    hit[:9, :4, 7] = hit[9:, 4:, 64] = True
+    assert not torch.isfinite(got[torch.from_numpy(hit).cuda()]).any()
+    check(got[torch.from_numpy(~hit).cuda()], want[~hit], spread[~hit], od)
+
+
+@gpu
 def test_two_streams_graph_and_backgrounds():
     """Two calls at once with workspaces of their own, and a captured one replayed on other inputs."""
     w, q, starts, sees, mask, most = make("int8", "per_token_head", "bf16", 16, 2, 128, 16, [3000, 1200, 64], [16, 3, 9])
